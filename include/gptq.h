@@ -349,6 +349,104 @@ int gptq_gemm_wqa16(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, con
                     const float* scales, const uint8_t* zeros, int32_t N, int32_t K, int32_t group, int32_t bits,
                     float* Y, int64_t ldy);
 
+/* Serving operators: what a layer runs between its quantised products when it
+ * answers token by token.  (The pages stop at the quantised weights' matrix
+ * products; these operators have no counterpart there.)  All ASYNC on the
+ * context's stream; device buffers, caller-owned.  Element types of x, y, K
+ * and V: GPTQ_BF16 (bit patterns) or GPTQ_F32; their last dimension (the head)
+ * is contiguous, the strides of tokens and heads are given in elements. */
+#define GPTQ_BF16 0
+#define GPTQ_F32 1
+#define GPTQ_ROPE_HALF 0        /* pairs (i, i + rot/2) */
+#define GPTQ_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1) */
+#define GPTQ_ROPE_PLAIN 0  /* frequencies base^(-2i/rot) */
+#define GPTQ_ROPE_LINEAR 1 /* all divided by factor */
+#define GPTQ_ROPE_BASE 2   /* base times factor^(rot/(rot-2)) */
+#define GPTQ_ROPE_PARTS 3  /* by turns over `original` positions: below `low` turns divided by
+                              factor, above `high` kept, in between mixed in proportion */
+
+typedef struct {
+  int32_t kind;     /* GPTQ_ROPE_PLAIN .. GPTQ_ROPE_PARTS */
+  int32_t original; /* length the frequencies were made for (parts) */
+  double factor, low, high;
+  double magnitude; /* both halves of the table are multiplied by it */
+} gptq_rope_scaling;
+
+/* Rotary table[length][2][rot/2] fp32: magnitude * cos and magnitude * sin of
+ * position * frequency, angles in fp64.  rot even, at most 256; scaling [host]
+ * may be NULL (plain, magnitude 1). */
+int gptq_rope_table(gptq_ctx ctx, int32_t length, int32_t rot, double base, const gptq_rope_scaling* scaling,
+                    float* table);
+
+/* Rotary positions: every pair (a, b) of the first rot of dim values of
+ * x[tokens][heads][dim] becomes (a c - b s, b c + a s) with c, s from the
+ * table's row positions[token]; the other values are copied.  inverse != 0
+ * turns back (s negated), which is also the gradient.  fp32 arithmetic,
+ * rounded once to y's type.  A position outside 0..length-1 gives NaN in the
+ * rotated part.  y may be x itself (same type and strides), else they must
+ * not overlap.  rot and dim even; rot == 0 copies. */
+int gptq_rope(gptq_ctx ctx, const void* x, int32_t x_type, int64_t tokens, int32_t heads, int32_t dim,
+              int64_t x_token, int64_t x_head, const int32_t* positions, const float* table, int32_t length,
+              int32_t rot, int32_t layout, int32_t inverse, void* y, int32_t y_type, int64_t y_token,
+              int64_t y_head);
+
+/* A paged key/value cache on min-max grids of 4 or 8 bits.  A slot is
+ * page_number * page + offset.  With rb = dim bits / 8:
+ *   k_codes[pages][heads][page][rb]: a token's codes side by side (4 bits:
+ *     code 2i in the low half of byte i, code 2i + 1 in the high half, as
+ *     gptq_pack_codes packs a row);
+ *   v_codes[pages][heads][rb][page]: the tokens of a page side by side (4
+ *     bits: byte row j holds dimension j in the low half, j + dim/2 in the high);
+ *   scales fp32 and zeros uint8 [pages][heads][page]: one grid for every
+ *     (token, head) of K and of V, value = scale * (code - zero).
+ * dim 64, 96, 128, 192 or 256; page a power of two from 16 to 256; pages * page
+ * < 2^31; buffers 16-byte aligned. */
+typedef struct {
+  uint8_t* k_codes;
+  float* k_scales;
+  uint8_t* k_zeros;
+  uint8_t* v_codes;
+  float* v_scales;
+  uint8_t* v_zeros;
+  int32_t pages, heads, page, dim, bits;
+  int32_t pad0;
+} gptq_kv_cache;
+
+/* Quantise K[tokens][heads][dim] and V into the cache: token t goes to
+ * slots[t] (a slot outside the pool: the token is skipped; the same slot
+ * twice in one call: undefined contents).  Per row v, in fp32 steps as
+ * gptq_quantize_lowrank: lo = min(min v, 0), hi = max(max v, 0), s = (hi - lo)
+ * / maxq, r = 1/s, z = clamp(rne(-lo r)), q = clamp(rne(fl32(fl32(v r) + z))).
+ * A range below 2^-100 is stored as zeros (s = 1); a row with a non-finite
+ * value, or whose range overflows, reads back as NaN.  Rows aligned to four
+ * values (else GPTQ_ERR_UNSUPPORTED). */
+int gptq_kv_write(gptq_ctx ctx, const gptq_kv_cache* cache, const void* K, const void* V, int32_t type,
+                  int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                  const int32_t* slots);
+
+/* Read back: K[t], V[t] = fl32(s (q - z)) of slots[t], rounded once to the
+ * type; zeros for a slot outside the pool.  Alignment as gptq_kv_write. */
+int gptq_kv_read(gptq_ctx ctx, const gptq_kv_cache* cache, const int32_t* slots, int64_t tokens, void* K,
+                 void* V, int32_t type, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head);
+
+/* Attention of the drafted tokens of every sequence over its cache:
+ *   O[b][t][hq] = sum_j softmax_j(scale Q[b][t][hq] . Khat[j]) Vhat[j]
+ * over the positions j of sequence b that token t sees: all j < lengths[b]
+ * (the tokens before the drafted ones), and of the drafted tokens, which lie
+ * at positions lengths[b] .. lengths[b] + tokens - 1, those whose bit is set in
+ * mask[b][t][words] (bit i in word i / 32; itself only if its own bit is set),
+ * or the first t + 1 without a mask (a chain; tokens = 1: one next token).
+ * Position j lies in page tables[b][j / page].  Positions past the table's
+ * width and those whose page number is outside the pool are not seen; a row
+ * that sees nothing is zero, as is every row of a sequence with lengths < 0.
+ * Query head hq reads cache head hq / (heads / cache.heads).  Q and O bf16
+ * bits; scores, softmax and sums in fp32 (see the kernel for its operands).
+ * Rows of Q 16-byte aligned, rows of O 8-byte aligned. */
+int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t* Q, int32_t seqs, int32_t tokens,
+                        int32_t heads, int64_t q_seq, int64_t q_token, int64_t q_head, const int32_t* tables,
+                        int32_t width, const int32_t* lengths, const uint32_t* mask, int32_t words, float scale,
+                        uint16_t* O, int64_t o_seq, int64_t o_token, int64_t o_head);
+
 /* Measurement support (not part of the method).  gptq_timing(ctx, kernels)
  * clears the totals and from then on brackets each launch of the named
  * kernels with a pair of HIP events on the context's stream.  kernels [host]
@@ -364,7 +462,9 @@ int gptq_gemm_wqa16(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, con
  * two-sided rounding k_r2d_unit, k_r2d_fill, k_r2d_tile, k_r2d_push, k_r2d_obj,
  * and for the quantised-input target k_qr_prep, k_qr_out, and for the
  * deployable outputs k_pack, k_unpack, k_lr_quant, k_gemm_w4a16,
- * k_gemv_w4a16 (4-bit codes), k_gemm_wqa16, k_gemv_wqa16 (other widths).
+ * k_gemv_w4a16 (4-bit codes), k_gemm_wqa16, k_gemv_wqa16 (other widths), and
+ * for the serving operators k_rope_table, k_rope, k_kv_write, k_kv_read,
+ * k_tree_attn.
  * gptq_kernel_time
  * waits for the recorded events and returns the summed elapsed milliseconds
  * and the number of timed launches of kernel `name` (0 and 0 if none).  Each

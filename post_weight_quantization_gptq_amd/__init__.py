@@ -15,6 +15,7 @@ import os
 __all__ = [
     "GPTQError",
     "Context",
+    "KVCache",
     "library_path",
     "load_library",
     "exported_symbols",
@@ -74,6 +75,38 @@ class _Layer(ctypes.Structure):
     ]
 
 
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("original", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+    ]
+
+
+class _KV(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("k_zeros", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("v_zeros", ctypes.c_void_p),
+        ("pages", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("pad0", ctypes.c_int32),
+    ]
+
+
+_ROPE_KINDS = {"linear": 1, "base": 2, "parts": 3}
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
 def load_library(path: str | None = None):
     """Load the HIP library (once).  Raises if it has not been built."""
     global _lib
@@ -113,6 +146,13 @@ def load_library(path: str | None = None):
     L.gptq_quantize_lowrank.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     L.gptq_gemm_w4a16.argtypes = [vp, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, i64]
     L.gptq_gemm_wqa16.argtypes = [vp, vp, i64, i64, vp, vp, vp, i32, i32, i32, i32, vp, i64]
+    kv = ctypes.POINTER(_KV)
+    L.gptq_rope_table.argtypes = [vp, i32, i32, d, ctypes.POINTER(_RopeScaling), vp]
+    L.gptq_rope.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, vp, vp, i32, i32, i32, i32, vp, i32, i64, i64]
+    L.gptq_kv_write.argtypes = [vp, kv, vp, vp, i32, i64, i64, i64, i64, i64, vp]
+    L.gptq_kv_read.argtypes = [vp, kv, vp, i64, vp, vp, i32, i64, i64, i64, i64]
+    L.gptq_tree_attention.argtypes = [vp, kv, vp, i32, i32, i32, i64, i64, i64, vp, i32, vp, vp, i32,
+                                      ctypes.c_float, vp, i64, i64, i64]
     L.gptq_quantize_batched.argtypes = [vp, i32, ctypes.POINTER(_Layer)]
     L.gptq_timing.argtypes = [vp, ctypes.c_char_p]
     L.gptq_kernel_time.argtypes = [vp, ctypes.c_char_p, ctypes.POINTER(d), ctypes.POINTER(i64)]
@@ -120,6 +160,7 @@ def load_library(path: str | None = None):
                  "gptq_quantize_noalloc", "gptq_lora", "gptq_lora_refine", "gptq_hessian64", "gptq_olrc", "gptq_bid_up", "gptq_round_2d",
                  "gptq_quantize_qronos", "gptq_cross_gram", "gptq_pack_codes", "gptq_unpack_codes",
                  "gptq_quantize_lowrank", "gptq_gemm_w4a16", "gptq_gemm_wqa16",
+                 "gptq_rope_table", "gptq_rope", "gptq_kv_write", "gptq_kv_read", "gptq_tree_attention",
                  "gptq_quantize_batched", "gptq_timing", "gptq_kernel_time"):
         getattr(L, name).restype = ctypes.c_int
     if path is None:
@@ -138,6 +179,40 @@ def exported_symbols(header: str | None = None):
 
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+
+
+class KVCache:
+    """A paged key/value cache on 4- or 8-bit grids: the six tensors of
+    gptq_kv_cache (checked here, once), which it keeps alive.
+
+    ``k_codes`` uint8 [pages, heads, page, dim*bits/8], ``v_codes`` uint8
+    [pages, heads, dim*bits/8, page], ``k_scales``/``v_scales`` float32 and
+    ``k_zeros``/``v_zeros`` uint8 [pages, heads, page]."""
+
+    FIELDS = ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales", "v_zeros")
+
+    def __init__(self, bits: int, k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros):
+        import torch
+        bits = int(bits)
+        if bits not in (4, 8):
+            raise ValueError("a cache holds 4 or 8 bits")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page, dim*bits/8]")
+        pages, heads, page, rb = k_codes.shape
+        shapes = dict(k_codes=(pages, heads, page, rb), v_codes=(pages, heads, rb, page))
+        given = (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)
+        for name, t in zip(self.FIELDS, given):
+            dtype = torch.float32 if name.endswith("scales") else torch.uint8
+            if t.device != k_codes.device or t.device.type != "cuda":
+                raise ValueError("%s must be on the cache's GPU" % name)
+            if t.dtype != dtype:
+                raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+            if tuple(t.shape) != shapes.get(name, (pages, heads, page)) or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous %s" % (name, list(shapes.get(name, (pages, heads, page)))))
+            setattr(self, name, t)
+        self.bits, self.pages, self.heads, self.page, self.dim = bits, pages, heads, page, rb * 8 // bits
+        self.device = k_codes.device
+        self._c = _KV(*[t.data_ptr() for t in given], pages, heads, page, self.dim, bits, 0)
 
 
 class Context:
@@ -524,6 +599,182 @@ class Context:
         self._check(self.lib.gptq_gemm_wqa16(self.handle, _ptr(X), M, X.stride(0), _ptr(packed), _ptr(scales),
                                              _ptr(zeros), N, K, int(group), int(bits), _ptr(Y), Y.stride(0)))
         return Y
+
+    # ------------------------------------------------------ serving operators
+    def _here(self, tensors, cache=None):
+        """With another torch stream current than the context's, tell the allocator that the
+        call's tensors are used on the context's stream."""
+        torch = self.torch
+        if torch.cuda.current_stream(self.device).cuda_stream != self.stream.cuda_stream:
+            if cache is not None:
+                tensors += tuple(getattr(cache, name) for name in KVCache.FIELDS)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def _empty(self, shape, dtype):
+        """An output tensor whose memory belongs to the context's stream."""
+        torch = self.torch
+        if torch.cuda.current_stream(self.device).cuda_stream == self.stream.cuda_stream:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _type(self, dtype, name):
+        torch = self.torch
+        if dtype is torch.bfloat16:
+            return 0
+        if dtype is torch.float32:
+            return 1
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, dtype))
+
+    def _rows(self, t, ndim, name):
+        """t as rows [..., heads, dim] with the last dimension contiguous."""
+        if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+            raise ValueError("%s must have %d dimensions, the last of them contiguous" % (name, ndim))
+        if t.device != self.device:
+            raise ValueError("%s must be on %s" % (name, self.device))
+        return t
+
+    def _cache(self, cache):
+        if not isinstance(cache, KVCache):
+            raise TypeError("cache must be a KVCache")
+        if cache.device != self.device:
+            raise ValueError("the cache must be on %s" % self.device)
+        return ctypes.byref(cache._c)
+
+    def kv_cache(self, pages: int, heads: int, dim: int, bits: int = 8, page: int = 64):
+        """A new KVCache of `pages` pages of `page` tokens (contents undefined until written)."""
+        torch = self.torch
+        if int(bits) not in (4, 8) or dim not in (64, 96, 128, 192, 256) or page not in (16, 32, 64, 128, 256):
+            raise ValueError("a cache needs 4 or 8 bits, dim 64, 96, 128, 192 or 256, page a power of two in 16..256")
+        rb = dim * int(bits) // 8
+        grid = (pages, heads, page)
+        return KVCache(bits, self._empty((pages, heads, page, rb), torch.uint8), self._empty(grid, torch.float32),
+                       self._empty(grid, torch.uint8), self._empty((pages, heads, rb, page), torch.uint8),
+                       self._empty(grid, torch.float32), self._empty(grid, torch.uint8))
+
+    def rope_table(self, length: int, rot: int, base: float = 10000.0, scaling: dict | None = None):
+        """Rotary table fp32 [length, 2, rot/2] (cos, sin).  scaling: dict(kind="linear" | "base" | "parts",
+        factor, and for parts original, low (default 1), high (default 32); optional magnitude)."""
+        sc = None
+        if scaling is not None:
+            s = dict(scaling)
+            kind = s.pop("kind", None)
+            if kind is not None and kind not in _ROPE_KINDS:
+                raise ValueError("scaling kind must be one of %s" % sorted(_ROPE_KINDS))
+            unknown = set(s) - {"factor", "original", "low", "high", "magnitude"}
+            if unknown:
+                raise ValueError("unknown scaling entries %s" % sorted(unknown))
+            sc = _RopeScaling(_ROPE_KINDS.get(kind, 0), int(s.get("original", 0)), float(s.get("factor", 1.0)),
+                              float(s.get("low", 1.0)), float(s.get("high", 32.0)), float(s.get("magnitude", 1.0)))
+        table = self._empty((int(length), 2, int(rot) // 2), self.torch.float32)
+        self._check(self.lib.gptq_rope_table(self.handle, int(length), int(rot), float(base),
+                                             ctypes.byref(sc) if sc is not None else None, table.data_ptr()))
+        return table
+
+    def rope(self, x, positions, table, layout: str = "half", inverse: bool = False, out=None, out_dtype=None):
+        """Rotary positions of x [tokens, heads, dim] (bf16 or fp32) by the rows `positions` (int32) of a
+        rope_table; the first 2 * table.shape[2] values of a head are turned, the rest copied.  `out` may be
+        x itself; otherwise a new tensor of out_dtype (default: x's)."""
+        torch = self.torch
+        x = self._rows(x, 3, "x")
+        tokens, heads, dim = x.shape
+        if layout not in _ROPE_LAYOUTS:
+            raise ValueError("layout must be 'half' or 'interleaved'")
+        self._dev(table, torch.float32, "table")
+        self._dev(positions, torch.int32, "positions")
+        if table.dim() != 3 or table.shape[1] != 2 or 2 * table.shape[2] > dim:
+            raise ValueError("table must be [length, 2, rot/2] with rot at most the head size")
+        if positions.shape != (tokens,):
+            raise ValueError("positions must hold one entry per token")
+        if out is None:
+            out = self._empty((tokens, heads, dim), x.dtype if out_dtype is None else out_dtype)
+        elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must have x's shape and the output type")
+        self._rows(out, 3, "out")
+        self._here((x, positions, table, out))
+        self._check(self.lib.gptq_rope(
+            self.handle, x.data_ptr(), self._type(x.dtype, "x"), tokens, heads, dim, x.stride(0), x.stride(1),
+            positions.data_ptr(), table.data_ptr(), table.shape[0], 2 * table.shape[2], _ROPE_LAYOUTS[layout],
+            int(bool(inverse)), out.data_ptr(), self._type(out.dtype, "out"), out.stride(0), out.stride(1)))
+        return out
+
+    def kv_write(self, cache, k, v, slots):
+        """Quantise k and v [tokens, heads, dim] (both bf16 or both fp32) into the cache at `slots` (int32,
+        page * cache.page + offset; negative: skipped)."""
+        c = self._cache(cache)
+        k, v = self._rows(k, 3, "k"), self._rows(v, 3, "v")
+        tokens = k.shape[0]
+        if k.shape != (tokens, cache.heads, cache.dim) or v.shape != k.shape:
+            raise ValueError("k and v must be [tokens, %d, %d]" % (cache.heads, cache.dim))
+        if v.dtype != k.dtype:
+            raise TypeError("k and v must have the same type")
+        self._dev(slots, self.torch.int32, "slots")
+        if slots.shape != (tokens,):
+            raise ValueError("slots must hold one entry per token")
+        self._here((k, v, slots), cache)
+        self._check(self.lib.gptq_kv_write(self.handle, c, k.data_ptr(), v.data_ptr(), self._type(k.dtype, "k"), tokens,
+                                           k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr()))
+
+    def kv_read(self, cache, slots, dtype=None, k=None, v=None):
+        """(k, v) [tokens, heads, dim] of the tokens at `slots`, as bf16 (default) or fp32; zeros for slots
+        outside the pool."""
+        torch = self.torch
+        c = self._cache(cache)
+        self._dev(slots, torch.int32, "slots")
+        if slots.dim() != 1:
+            raise ValueError("slots must have one dimension")
+        shape = (slots.shape[0], cache.heads, cache.dim)
+        dtype = dtype if dtype is not None else k.dtype if k is not None else torch.bfloat16
+        kind = self._type(dtype, "dtype")
+        k = self._empty(shape, dtype) if k is None else self._rows(k, 3, "k")
+        v = self._empty(shape, dtype) if v is None else self._rows(v, 3, "v")
+        if k.shape != shape or v.shape != shape or k.dtype != dtype or v.dtype != dtype:
+            raise ValueError("k and v must be %s of %s" % (list(shape), dtype))
+        self._here((slots, k, v), cache)
+        self._check(self.lib.gptq_kv_read(self.handle, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), kind,
+                                          k.stride(0), k.stride(1), v.stride(0), v.stride(1)))
+        return k, v
+
+    def tree_attention(self, q, cache, tables, lengths, mask=None, scale: float | None = None, out=None):
+        """Attention of q [seqs, tokens, heads, dim] (bf16), the drafted tokens of each sequence, over the cache.
+
+        tables int32 [seqs, width]: page numbers; lengths int32 [seqs]: tokens before the drafted ones, whose keys
+        and values lie at the next positions; mask int32 [seqs, tokens, words]: bit i of row t says whether
+        drafted token t sees drafted token i (None: a chain).  scale defaults to dim ** -0.5.  bf16 result."""
+        torch = self.torch
+        c = self._cache(cache)
+        q = self._rows(q, 4, "q")
+        seqs, tokens, heads, dim = q.shape
+        if q.dtype is not torch.bfloat16:
+            raise TypeError("q must be bfloat16")
+        if dim != cache.dim or heads % cache.heads:
+            raise ValueError("q must have heads a multiple of %d and dim %d" % (cache.heads, cache.dim))
+        self._dev(tables, torch.int32, "tables")
+        self._dev(lengths, torch.int32, "lengths")
+        if tables.dim() != 2 or tables.shape[0] != seqs or lengths.shape != (seqs,):
+            raise ValueError("tables must be [seqs, width] and lengths [seqs]")
+        words = 0
+        if mask is not None:
+            self._dev(mask, torch.int32, "mask")
+            if mask.dim() != 3 or mask.shape[0] != seqs or mask.shape[1] != tokens:
+                raise ValueError("mask must be [seqs, tokens, words]")
+            words = mask.shape[2]
+            if 32 * words < tokens:  # (an empty tensor's null pointer would mean a chain)
+                raise GPTQError(1, "a mask row has too few words")
+        if out is None:
+            out = self._empty(q.shape, torch.bfloat16)
+        elif out.shape != q.shape or out.dtype is not torch.bfloat16:
+            raise ValueError("out must be bfloat16 of q's shape")
+        self._rows(out, 4, "out")
+        self._here((q, tables, lengths, mask, out), cache)
+        self._check(self.lib.gptq_tree_attention(
+            self.handle, c, q.data_ptr(), seqs, tokens, heads, q.stride(0), q.stride(1), q.stride(2),
+            tables.data_ptr(), tables.shape[1], lengths.data_ptr(), mask.data_ptr() if mask is not None else None, words,
+            dim ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0), out.stride(1),
+            out.stride(2)))
+        return out
 
     def quantize_batched(self, layers):
         """layers: list of dicts with W, bits, group, block, lam_rel (and X or H, optional lam_abs,

@@ -18,6 +18,7 @@
 #include "launch.h"
 #include "plan.h"
 #include "planner.h"
+#include "serve.h"
 
 #define GPTQ_API extern "C" __attribute__((visibility("default")))
 
@@ -1330,4 +1331,211 @@ GPTQ_API int gptq_gemm_wqa16(gptq_ctx c, const uint16_t* X, int64_t M, int64_t l
                              const float* scales, const uint8_t* zeros, int32_t N, int32_t K, int32_t group,
                              int32_t bits, float* Y, int64_t ldy) {
   return gemm_wq(c, X, M, ldx, packed, scales, zeros, N, K, group, bits, Y, ldy);
+}
+
+// ------------------------------------------------------ serving operators --
+GPTQ_API int gptq_rope_table(gptq_ctx c, int32_t length, int32_t rot, double base, const gptq_rope_scaling* sc,
+                             float* table) {
+  if (!c) return GPTQ_ERR_INVALID_ARG;
+  c->err.clear();
+  if (length < 0 || rot < 0 || rot % 2 != 0) return set_err(c, GPTQ_ERR_INVALID_ARG, "bad table size");
+  if (rot > 256) return set_err(c, GPTQ_ERR_UNSUPPORTED, "a rotary width above 256");
+  if (!(base > 0.0) || !std::isfinite(base)) return set_err(c, GPTQ_ERR_INVALID_ARG, "the base must be positive");
+  const gptq_rope_scaling none{GPTQ_ROPE_PLAIN, 0, 1.0, 1.0, 1.0, 1.0};
+  const gptq_rope_scaling s = sc ? *sc : none;
+  if (s.kind < GPTQ_ROPE_PLAIN || s.kind > GPTQ_ROPE_PARTS || !std::isfinite(s.factor) || !std::isfinite(s.magnitude))
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "bad rotary scaling");
+  if (s.kind != GPTQ_ROPE_PLAIN && !(s.factor > 0.0))
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "the scaling factor must be positive");
+  if (s.kind == GPTQ_ROPE_PARTS && !(s.original > 0 && s.low >= 0.0 && s.high > s.low && std::isfinite(s.high)))
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "scaling by parts needs original > 0 and 0 <= low < high");
+  if (s.kind == GPTQ_ROPE_BASE && rot == 2)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "scaling the base needs more than one pair");
+  if (length == 0 || rot == 0) return GPTQ_OK;
+  if (!table) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if (s.kind == GPTQ_ROPE_BASE) base *= std::pow(s.factor, (double)rot / (rot - 2));
+  RopeFreq f{};
+  for (int i = 0; i < rot / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / rot);
+    if (s.kind == GPTQ_ROPE_LINEAR) w /= s.factor;
+    if (s.kind == GPTQ_ROPE_PARTS) {
+      const double turns = s.original * w / (2.0 * M_PI);
+      const double keep = std::min(1.0, std::max(0.0, (turns - s.low) / (s.high - s.low)));
+      w *= keep + (1.0 - keep) / s.factor;
+    }
+    f.f[i] = w;
+  }
+  DeviceGuard g(c->device);
+  LAUNCH(c, "k_rope_table", launch_rope_table(f, length, rot / 2, s.magnitude, table, c->stream));
+  return GPTQ_OK;
+}
+
+static bool bad_type(int32_t t) { return t != GPTQ_BF16 && t != GPTQ_F32; }
+
+GPTQ_API int gptq_rope(gptq_ctx c, const void* x, int32_t x_type, int64_t tokens, int32_t heads, int32_t dim,
+                       int64_t x_token, int64_t x_head, const int32_t* positions, const float* table, int32_t length,
+                       int32_t rot, int32_t layout, int32_t inverse, void* y, int32_t y_type, int64_t y_token,
+                       int64_t y_head) {
+  if (!c) return GPTQ_ERR_INVALID_ARG;
+  c->err.clear();
+  if (tokens < 0 || heads < 0 || dim < 0 || length < 0) return set_err(c, GPTQ_ERR_INVALID_ARG, "negative size");
+  if (rot < 0 || rot > dim || rot % 2 != 0 || dim % 2 != 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "the rotary width must be even, in an even head size");
+  if (bad_type(x_type) || bad_type(y_type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
+  if (layout != GPTQ_ROPE_HALF && layout != GPTQ_ROPE_INTERLEAVED)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown rotary layout");
+  if (x_token < 0 || x_head < 0 || y_token < 0 || y_head < 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "negative stride");
+  if (tokens == 0 || heads == 0 || dim == 0) return GPTQ_OK;
+  if (!x || !y || (rot > 0 && (!positions || !table || length == 0)))
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if (tokens > INT32_MAX || tokens * heads > ((int64_t)1 << 39) / dim)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many values for one launch");
+  // the stride of a dimension of one is never used
+  if (tokens == 1) x_token = y_token = 0;
+  if (heads == 1) x_head = y_head = 0;
+  DeviceGuard g(c->device);
+  RopeProb p{x, y, positions, table, tokens, x_token, x_head, y_token, y_head, heads, dim, rot, length,
+             inverse ? -1.f : 1.f};
+  LAUNCH(c, "k_rope", launch_rope(p, x_type, y_type, layout, c->stream));
+  return GPTQ_OK;
+}
+
+// Checks of a cache descriptor; fills the kernels' view of it.
+static int check_cache(gptq_ctx c, const gptq_kv_cache* kv, KvPool& o) {
+  if (!kv) return set_err(c, GPTQ_ERR_INVALID_ARG, "null cache");
+  if (kv->pages < 1 || kv->heads < 1) return set_err(c, GPTQ_ERR_INVALID_ARG, "a cache needs pages and heads");
+  if (kv->bits != 4 && kv->bits != 8) return set_err(c, GPTQ_ERR_UNSUPPORTED, "a cache holds 4 or 8 bits");
+  if (kv->dim != 64 && kv->dim != 96 && kv->dim != 128 && kv->dim != 192 && kv->dim != 256)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "the head size must be 64, 96, 128, 192 or 256");
+  if (kv->page < 16 || kv->page > 256 || (kv->page & (kv->page - 1)) != 0)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "the page size must be a power of two from 16 to 256");
+  if ((int64_t)kv->pages * kv->page > INT32_MAX || kv->heads > 65535)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "cache too large for 32-bit slots");
+  if (!kv->k_codes || !kv->k_scales || !kv->k_zeros || !kv->v_codes || !kv->v_scales || !kv->v_zeros)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if (((uintptr_t)kv->k_codes | (uintptr_t)kv->k_scales | (uintptr_t)kv->k_zeros | (uintptr_t)kv->v_codes |
+       (uintptr_t)kv->v_scales | (uintptr_t)kv->v_zeros) & 15)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "the cache's buffers must be 16-byte aligned");
+  o = KvPool{kv->k_codes, kv->k_scales, kv->k_zeros, kv->v_codes, kv->v_scales, kv->v_zeros, kv->pages, kv->heads,
+             kv->dim, kv->dim * kv->bits / 8, __builtin_ctz((unsigned)kv->page)};
+  return GPTQ_OK;
+}
+
+// Rows of four values are read and written at once.
+static bool rows_of_4(const void* p, int32_t type, int64_t t, int64_t h) {
+  return t % 4 == 0 && h % 4 == 0 && (uintptr_t)p % (type == GPTQ_F32 ? 16 : 8) == 0;
+}
+
+GPTQ_API int gptq_kv_write(gptq_ctx c, const gptq_kv_cache* cache, const void* K, const void* V, int32_t type,
+                           int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                           const int32_t* slots) {
+  if (!c) return GPTQ_ERR_INVALID_ARG;
+  c->err.clear();
+  KvWriteProb p{};
+  int rc = check_cache(c, cache, p.c);
+  if (rc) return rc;
+  if (tokens < 0 || k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "negative size");
+  if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
+  if (tokens == 0) return GPTQ_OK;
+  if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
+  if (cache->heads == 1) k_head = v_head = 0;
+  if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "rows of K and V must be aligned to four values");
+  p.k = K;
+  p.v = V;
+  p.slots = slots;
+  p.tokens = tokens;
+  p.kt = k_token;
+  p.kh = k_head;
+  p.vt = v_token;
+  p.vh = v_head;
+  DeviceGuard g(c->device);
+  LAUNCH(c, "k_kv_write", launch_kv_write(p, type, cache->bits, c->stream));
+  return GPTQ_OK;
+}
+
+GPTQ_API int gptq_kv_read(gptq_ctx c, const gptq_kv_cache* cache, const int32_t* slots, int64_t tokens, void* K,
+                          void* V, int32_t type, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head) {
+  if (!c) return GPTQ_ERR_INVALID_ARG;
+  c->err.clear();
+  KvReadProb p{};
+  int rc = check_cache(c, cache, p.c);
+  if (rc) return rc;
+  if (tokens < 0 || k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "negative size");
+  if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
+  if (tokens == 0) return GPTQ_OK;
+  if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
+  if (cache->heads == 1) k_head = v_head = 0;
+  if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "rows of K and V must be aligned to four values");
+  p.k = K;
+  p.v = V;
+  p.slots = slots;
+  p.tokens = tokens;
+  p.kt = k_token;
+  p.kh = k_head;
+  p.vt = v_token;
+  p.vh = v_head;
+  DeviceGuard g(c->device);
+  LAUNCH(c, "k_kv_read", launch_kv_read(p, type, cache->bits, c->stream));
+  return GPTQ_OK;
+}
+
+GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const uint16_t* Q, int32_t seqs,
+                                 int32_t tokens, int32_t heads, int64_t q_seq, int64_t q_token, int64_t q_head,
+                                 const int32_t* tables, int32_t width, const int32_t* lengths, const uint32_t* mask,
+                                 int32_t words, float scale, uint16_t* O, int64_t o_seq, int64_t o_token,
+                                 int64_t o_head) {
+  if (!c) return GPTQ_ERR_INVALID_ARG;
+  c->err.clear();
+  AttnProb p{};
+  int rc = check_cache(c, cache, p.c);
+  if (rc) return rc;
+  if (seqs < 0 || tokens < 0 || heads < 0 || width < 0 || words < 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "negative size");
+  if (q_seq < 0 || q_token < 0 || q_head < 0 || o_seq < 0 || o_token < 0 || o_head < 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "negative stride");
+  if (heads % cache->heads != 0)
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "query heads must be a multiple of the cache's heads");
+  if (!std::isfinite(scale)) return set_err(c, GPTQ_ERR_INVALID_ARG, "non-finite scale");
+  if (seqs == 0 || tokens == 0 || heads == 0) return GPTQ_OK;
+  if (mask && (int64_t)words * 32 < tokens) return set_err(c, GPTQ_ERR_INVALID_ARG, "a mask row has too few words");
+  if (!Q || !O || !lengths || (width > 0 && !tables)) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
+  if ((int64_t)width * cache->page > INT32_MAX || (int64_t)tokens * heads > ((int64_t)1 << 26) ||
+      (int64_t)seqs * tokens * heads > INT32_MAX)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many rows or positions for one launch");
+  if (seqs == 1) q_seq = o_seq = 0;  // the stride of a dimension of one is never used
+  if (tokens == 1) q_token = o_token = 0;
+  if (heads == 1) q_head = o_head = 0;
+  if (q_seq % 8 || q_token % 8 || q_head % 8 || o_seq % 4 || o_token % 4 || o_head % 4 || (uintptr_t)Q % 16 ||
+      (uintptr_t)O % 8)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "rows of Q must be 16-byte aligned, rows of O 8-byte aligned");
+  p.q = Q;
+  p.o = O;
+  p.tables = tables;
+  p.lengths = lengths;
+  p.mask = mask;
+  p.qb = q_seq;
+  p.qt = q_token;
+  p.qh = q_head;
+  p.ob = o_seq;
+  p.ot = o_token;
+  p.oh = o_head;
+  p.seqs = seqs;
+  p.tokens = tokens;
+  p.heads = heads;
+  p.group = heads / cache->heads;
+  p.width = width;
+  p.words = words;
+  p.scale = scale * 1.4426950408889634f;
+  DeviceGuard g(c->device);
+  LAUNCH(c, "k_tree_attn", launch_tree_attn(p, cache->bits, c->stream));
+  return GPTQ_OK;
 }
