@@ -37,7 +37,7 @@ struct gptq_ctx_s {
   int ncu = 256;
   int nxcd = 8;
   std::string err;
-  DevBuf partials, xt, facA, facY, work, eblk, objp, dinv, slots, blob, lora, r2d, qr;
+  DevBuf partials, xt, facA, facY, work, eblk, objp, dinv, slots, blob, lora, r2d, qr, attn;
   void* hblob = nullptr;  // pinned staging for the task tables
   size_t hblob_cap = 0;
   void* hsmall = nullptr;  // pinned read-back area
@@ -660,7 +660,7 @@ GPTQ_API int gptq_destroy(gptq_ctx c) {
     (void)hipStreamSynchronize(c->stream);
     if (c->side) (void)hipStreamSynchronize(c->side);
     DevBuf* bufs[] = {&c->partials, &c->xt, &c->facA, &c->facY, &c->work, &c->eblk, &c->dinv,
-                      &c->objp, &c->slots, &c->blob, &c->lora, &c->r2d, &c->qr};
+                      &c->objp, &c->slots, &c->blob, &c->lora, &c->r2d, &c->qr, &c->attn};
     for (DevBuf* b : bufs)
       if (b->p) (void)hipFree(b->p);
     if (c->hblob) (void)hipHostFree(c->hblob);
@@ -1536,6 +1536,14 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   p.words = words;
   p.scale = scale * 1.4426950408889634f;
   DeviceGuard g(c->device);
+  plan_tree_attn(p, c->ncu);
+  if (p.nsplit > 1) {
+    const size_t rows = (size_t)seqs * tokens * heads * p.nsplit;
+    if ((rc = ensure(c, c->attn, rows * (cache->dim + 2) * sizeof(float)))) return rc;
+    p.part = (float*)c->attn.p;
+    p.ml = p.part + rows * cache->dim;
+  }
   LAUNCH(c, "k_tree_attn", launch_tree_attn(p, cache->bits, c->stream));
+  if (p.nsplit > 1) LAUNCH(c, "k_attn_join", launch_attn_join(p, c->stream));
   return GPTQ_OK;
 }

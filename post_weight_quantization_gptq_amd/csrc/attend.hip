@@ -2,87 +2,600 @@
 #include "common.h"
 #include "serve.h"
 
-// One wave per (sequence, token, query head): 64 positions at a time, one per
-// lane for the scores, then the lanes take dimensions for the weighted sum.
-template <int BITS>
-__global__ __launch_bounds__(64) void k_tree_attn(const AttnProb p) {
-  __shared__ float qs[256], pr[64];
-  __shared__ size_t row[64];
-  const KvPool& c = p.c;
-  const int lane = threadIdx.x, D = c.dim;
-  const int hq = blockIdx.x % p.heads, h = hq / p.group;
-  const int bt = blockIdx.x / p.heads, b = bt / p.tokens, t = bt % p.tokens;
-  const uint16_t* q = p.q + b * p.qb + t * p.qt + hq * p.qh;
-  for (int d = lane; d < D; d += 64) qs[d] = __builtin_bit_cast(float, (uint32_t)q[d] << 16);
-  const int len = p.lengths[b];
-  const long long cap = (long long)p.width << c.pshift;
-  const int n = len < 0 ? 0 : (int)min((long long)len + p.tokens, cap);
-  const int pm = (1 << c.pshift) - 1;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < n; j0 += 64) {
-    const int j = j0 + lane;
-    bool see = j < n;
-    if (see && j >= len)
-      see = p.mask ? (p.mask[(size_t)bt * p.words + ((j - len) >> 5)] >> ((j - len) & 31)) & 1u : j - len <= t;
-    float x = -INFINITY;
-    size_t at = 0;
-    if (see) {
-      const int page = p.tables[(size_t)b * p.width + (j >> c.pshift)];
-      see = (unsigned)page < (unsigned)c.pages;
-      if (see) {
-        at = (((size_t)page * c.heads + h) << c.pshift) + (j & pm);
-        const uint8_t* k = c.kc + at * c.rb;
-        const float z = (float)c.kz[at];
-        float a = 0.f;
-        for (int d = 0; d < D; ++d) {
-          const int code = BITS == 8 ? k[d] : (k[d >> 1] >> (4 * (d & 1))) & 15;
-          a += qs[d] * ((float)code - z);
-        }
-        x = a * c.ks[at] * p.scale;
-      }
-    }
-    float mt = x;
-    for (int o = 32; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor(mt, o));
-    const float mn = fmaxf(m, mt);
-    const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
-    const float e = see ? exp2f(x - mn) : 0.f;
-    l = l * al + e;
-    m = mn;
-    __syncthreads();
-    pr[lane] = see ? e * c.vs[at] : 0.f;
-    row[lane] = see ? at : (size_t)0;
-    __syncthreads();
-    for (int u = 0; u < 4; ++u) acc[u] *= al;
-    for (int i = 0; i < 64; ++i) {
-      const float w = pr[i];
-      if (w == 0.f) continue;
-      const size_t a = row[i];
-      const float z = (float)c.vz[a];
-      const uint8_t* vb = c.vc + ((a >> c.pshift) * c.rb << c.pshift) + (a & pm);
-      for (int u = 0; u < 4; ++u) {
-        const int d = lane + 64 * u;
-        if (d >= D) continue;
-        const int r = BITS == 8 || d < D / 2 ? d : d - D / 2;
-        const int by = vb[(size_t)r << c.pshift];
-        const int code = BITS == 8 ? by : (d < D / 2 ? by & 15 : by >> 4);
-        acc[u] += w * ((float)code - z);
-      }
-    }
-    __syncthreads();
+#include <type_traits>
+
+// running maximum of a row that has seen nothing (finite: its product with a zero scale is 0)
+#define NONE (-3.402823466e38f)
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+namespace {
+
+// Codes enter the matrix unit as float16 without a conversion: 0x6400 | c is
+// 1024 + c.  Two bytes of w, at bit 0 and 8 (half 0) or 16 and 24 (half 1):
+__device__ __forceinline__ uint32_t bytes2(uint32_t w, int half) {
+  return __builtin_amdgcn_perm(0x64646464u, w, half ? 0x04030402u : 0x04010400u);
+}
+// the nibbles at bits 0 and 16 as 1024 + c, and those at bits 4 and 20 as 1024 + 16 c
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w & 0x00F000F0u) | 0x64006400u; }
+
+// float16 pair c minus float16 pair z as a bfloat16 pair (exact for integers up to 256)
+__device__ __forceinline__ uint32_t diff_bf16(uint32_t c, uint32_t z) {
+  uint32_t lo, hi;
+  asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel_hi:[1,0,1]" : "=v"(lo) : "v"(c), "v"(z));
+  asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[1,0,1] op_sel_hi:[1,0,1]" : "=v"(hi) : "v"(c), "v"(z));
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+}
+// the leading 16 bits of two floats (their bfloat16 truncations), and those of what the truncation left
+__device__ __forceinline__ uint32_t lead16(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float rest16(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
+
+// largest value (sum) of the four lanes that differ in lane / 16
+__device__ __forceinline__ float max_groups(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+__device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_bf(const u32x4& a, const u32x4& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+__device__ __forceinline__ float up16(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
+
+// One tile of TP positions as a lane holds it: see k_tree_attn.
+template <int DIM, int BITS, int TP>
+struct Tile {
+  static constexpr int CH = TP / 4;          // positions whose weights a lane has: a chunk
+  static constexpr int NI = CH / 4;          // blocks of 16 key rows
+  static constexpr int NS = CH / 8;          // steps of 32 positions of the second product
+  static constexpr int RB = DIM * BITS / 8;  // bytes of a key row; byte rows of a value block
+  static constexpr int NW = RB / 16;         // words of a key row per lane
+  static constexpr int NF = RB / 64;         // ... whole 64-byte pieces
+  static constexpr bool R32 = RB % 64 >= 32, R16 = RB % 32 != 0;
+  static constexpr int NMB = RB / 16;        // blocks of 16 byte rows of values
+  typedef uint32_t Chunk __attribute__((ext_vector_type(NI)));
+  uint32_t k[NI][NW];
+  uint32_t v[NMB][NI];
+  float ks[CH], vs[CH];
+  uint32_t kz[NI], vz[NI];
+  bool bad;
+
+  // byte offset in a key row of word w of lane group g
+  static __device__ __forceinline__ constexpr int off(int w, int g) {
+    if (w < 4 * NF) return 64 * (w / 4) + 16 * g + 4 * (w % 4);
+    if (R32 && w < 4 * NF + 2) return 64 * NF + 8 * g + 4 * (w - 4 * NF);
+    return 64 * NF + (R32 ? 32 : 0) + 4 * g;
   }
-  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o);
-  uint16_t* out = p.o + b * p.ob + t * p.ot + hq * p.oh;
-  for (int u = 0; u < 4; ++u) {
-    const int d = lane + 64 * u;
-    if (d < D) out[d] = __builtin_bit_cast(uint16_t, (__bf16)(l == 0.f ? 0.f : acc[u] / l));
+};
+
+}  // namespace
+
+// Softmax attention in one pass over the cache with a running maximum and sum.
+//
+// A wave takes 16 NB query rows (token, head of the group) of one sequence and
+// key head, and TP = 64 or 32 positions at a time, and works with both products
+// transposed, so that nothing moves between lanes:
+//   S^T = K Q^T: 16 positions x 16 rows per MFMA, the key rows ordered so that
+//     the lane (g = lane / 16, n = lane % 16) receives row n's scores at
+//     chunk g of the tile (TP/4 consecutive positions), four for each MFMA;
+//   O^T = V^T P^T: the same lane's weights of those positions are its part of
+//     the P^T operand as they are, and the V^T operand is as many consecutive
+//     bytes of a dimension's row, which is why values lie dimension by
+//     dimension in a page.  Every register of the sum belongs to row n.
+// Codes enter as 1024 + c (or 1024 + 16 c) in float16, made with one byte
+// permutation or mask for two codes.  The offset leaves the scores through
+// the MFMA's initial value -1024 sum q and z sum q.  Values enter as c - z in
+// bfloat16 (exact).  All products are exact in float32.
+// Queries are scaled by a power of two per row to just below 2^15 (exact for
+// elements within 2^-29 of the largest) and exact in float16 (bf16 has 8 bits).
+//
+// Weights enter the second product times their position's scale, as two
+// bfloat16 numbers, the leading 8 bits and the next 8: with one of them the
+// weights' rounding would be as large as the result's, and float16's range
+// would lose the weights under 2^-29 of the largest, which are all there is
+// where the others' values are zero.
+//
+// Positions of a tile after the context or on a page outside the pool go
+// through the masked form, which takes invisible positions out of maximum,
+// sum and weights by selection, whatever their scales hold.
+//
+// The four waves of a workgroup take every fourth tile of its share of the
+// positions and are joined in LDS in a fixed order; with several shares
+// (nsplit) the unnormalised rows go to the workspace for k_attn_join.
+template <int DIM, int BITS, int NB, int TP, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
+  typedef Tile<DIM, BITS, TP> T;
+  constexpr int CH = T::CH, NI = T::NI, NS = T::NS;
+  constexpr int NK = DIM / 32, NO = DIM / 16, NMB = T::NMB;
+  __shared__ float sm[4][16 * NB], sl[4][16 * NB];
+  __shared__ f32x4 so[2][NB * NO][64];
+  const KvPool& c = p.c;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Blocks of one (sequence, key head, share) are eight apart: on one XCD,
+  // whose L2 then holds the share's codes for all of them.
+  const int x = blockIdx.x / (8 * p.nrb), rem = blockIdx.x % (8 * p.nrb);
+  const int rb = rem >> 3, unit = 8 * x + (rem & 7);
+  if (unit >= p.seqs * c.heads * p.nsplit) return;
+  const int split = unit % p.nsplit, bh = unit / p.nsplit;
+  const int h = bh % c.heads, b = bh / c.heads;
+  const int R = p.tokens * p.group;
+
+  const int len = p.lengths[b];
+  const int cap = p.width << c.pshift;
+  const int npos = len < 0 ? 0 : (int)min((long long)len + p.tokens, (long long)cap);
+  const int ntile = (npos + TP - 1) / TP;
+  const int per = (ntile + p.nsplit - 1) / p.nsplit;
+  const int t1 = min(ntile, (split + 1) * per);
+  int tile = split * per + w;
+
+  // queries: row n of block nb
+  u32x4 qf[NB][NK];
+  float qs0[NB], qs1[NB], cq[NB];
+  int tok[NB];
+  const float asc = fabsf(p.scale);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int rr = 16 * (NB * rb + nb) + n;
+    const int t = min(rr, R - 1) / p.group, hq = h * p.group + min(rr, R - 1) % p.group;
+    tok[nb] = t;
+    const uint16_t* q = p.q + b * p.qb + t * p.qt + hq * p.qh;
+    float v[NK][8];
+    float mx = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = BITS == 8 ? T::off(2 * ks + (e >> 2), g) + (e & 3) : 2 * T::off(ks, g) + (e >> 1) + 4 * (e & 1);
+        const float f = __uint_as_float((uint32_t)q[d] << 16);
+        v[ks][e] = rr < R ? f : 0.f;
+        mx = fmaxf(mx, fabsf(v[ks][e]));
+      }
+    }
+    mx = max_groups(mx);
+    const int ex = (int)(__float_as_uint(mx) >> 23);
+    const int sh = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^sh max in [2^14, 2^15)
+    const float up = __uint_as_float((uint32_t)(127 + sh) << 23), sgn = p.scale < 0.f ? -up : up;
+    cq[nb] = asc * __uint_as_float((uint32_t)(127 - sh) << 23);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // 4 bits: the odd codes of a word arrive times 16
+        const float f = BITS == 4 && (j & 1) ? sgn * 0.0625f : sgn;
+        o[j] = pack16(v[ks][2 * j] * f, v[ks][2 * j + 1] * f);
+        const float u = up16(o[j] & 0xFFFF) + up16(o[j] >> 16);
+        s1 += u;
+        s0 += BITS == 4 && (j & 1) ? 16.f * u : u;
+      }
+      qf[nb][ks] = u32x4{o[0], o[1], o[2], o[3]};
+    }
+    qs0[nb] = sum_groups(s0);
+    qs1[nb] = -1024.f * sum_groups(s1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  f32x4 acc[NB][NO];
+  float M[NB], l[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    M[nb] = NONE;
+    l[nb] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NO; ++i) acc[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int pm = (1 << c.pshift) - 1, lastchunk = max(npos - 1, 0) / CH;
+  const int* table = p.tables + (size_t)b * p.width;
+  // page of a chunk (of the last one there is for those past the end)
+  auto page_of = [&](int chunk, bool& bad) {
+    const int pg = glb(table)[(min(chunk, lastchunk) * CH) >> c.pshift];
+    bad = (unsigned)pg >= (unsigned)c.pages;
+    return bad ? 0 : pg;
+  };
+  // pages of the tile to be loaded next: of the lane's key rows, of its chunk
+  struct Pages {
+    int k, v;
+    bool bk, bv;
+  };
+  auto find = [&](int tl) {
+    Pages q;
+    q.k = page_of(4 * tl + (n >> 2), q.bk);
+    q.v = page_of(4 * tl + g, q.bv);
+    return q;
+  };
+  auto load_k = [&](T& t, int tl, const Pages& q) {
+    const size_t pk = (size_t)q.k * c.heads + h;
+    const int ok = (min(4 * tl + (n >> 2), lastchunk) * CH) & pm;
+    const uint8_t* kr = c.kc + ((pk << c.pshift) + ok + (n & 3)) * T::RB;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint8_t* r = kr + 4 * i * T::RB;
+#pragma unroll
+      for (int s = 0; s < T::NF; ++s) {
+        const u32x4 u = *glb((const u32x4*)(r + 64 * s + 16 * g));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.k[i][4 * s + e] = u[e];
+      }
+      if constexpr (T::R32) {
+        const u32x2 u = *glb((const u32x2*)(r + 64 * T::NF + 8 * g));
+        t.k[i][4 * T::NF] = u[0];
+        t.k[i][4 * T::NF + 1] = u[1];
+      }
+      if constexpr (T::R16) t.k[i][T::NW - 1] = *glb((const uint32_t*)(r + T::RB - 16 + 4 * g));
+    }
+  };
+  auto load_g = [&](T& t, int tl, const Pages& q) {
+    t.bad = q.bv;
+    const size_t at = (((size_t)q.v * c.heads + h) << c.pshift) + ((min(4 * tl + g, lastchunk) * CH) & pm);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const f32x4 a = *glb((const f32x4*)(c.ks + at + 4 * i)), e = *glb((const f32x4*)(c.vs + at + 4 * i));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        t.ks[4 * i + r] = a[r];
+        t.vs[4 * i + r] = e[r];
+      }
+    }
+    typedef typename T::Chunk Chunk;
+    const Chunk zk = *glb((const Chunk*)(c.kz + at)), zv = *glb((const Chunk*)(c.vz + at));
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      t.kz[i] = zk[i];
+      t.vz[i] = zv[i];
+    }
+  };
+  auto load_v = [&](T& t, int tl, const Pages& q) {
+    const size_t pv = (size_t)q.v * c.heads + h;
+    const uint8_t* vr = c.vc + ((pv * T::RB + n) << c.pshift) + ((min(4 * tl + g, lastchunk) * CH) & pm);
+#pragma unroll
+    for (int i = 0; i < NMB; ++i) {
+      typedef typename T::Chunk Chunk;
+      const Chunk u = *glb((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
+#pragma unroll
+      for (int e = 0; e < NI; ++e) t.v[i][e] = u[e];
+    }
+  };
+
+  // which of the positions j0 .. j0 + CH - 1 does drafted token t see
+  auto seen = [&](int j0, int t) -> uint32_t {
+    const int below = min(max(len - j0, 0), CH);
+    uint32_t bits;
+    if (p.mask) {
+      bits = 0;
+      const int i0 = max(j0 - len, 0), wd = i0 >> 5;
+      const uint32_t* m = p.mask + ((size_t)b * p.tokens + t) * p.words;
+      if (below < CH) {
+        const uint64_t lo = wd < p.words ? m[wd] : 0u, hi = wd + 1 < p.words ? m[wd + 1] : 0u;
+        bits = (uint32_t)((hi << 32 | lo) >> (i0 & 31));
+      }
+      bits = bits << below | ((1u << below) - 1u);
+    } else {
+      bits = (1u << min(max(len + t + 1 - j0, 0), CH)) - 1u;
+    }
+    return bits & ((1u << min(max(npos - j0, 0), CH)) - 1u);
+  };
+
+  f32x4 S[NB][NI];
+  u32x4 P[NB][2][NS];  // [leading, next][step]
+  auto scores = [&](const T& t) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb][i] = f32x4{qs1[nb], qs1[nb], qs1[nb], qs1[nb]};
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        u32x4 a;
+        if constexpr (BITS == 8) {
+          const uint32_t w0 = t.k[i][2 * ks], w1 = t.k[i][2 * ks + 1];
+          a = u32x4{bytes2(w0, 0), bytes2(w0, 1), bytes2(w1, 0), bytes2(w1, 1)};
+        } else {
+          const uint32_t w0 = t.k[i][ks], w8 = w0 >> 8;
+          a = u32x4{nib_lo(w0), nib_hi(w0), nib_lo(w8), nib_hi(w8)};
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, qf[nb][ks], S[nb][i]);
+      }
+      if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto weights = [&](const T& t, int tl) {
+    const bool masked = TP * (tl + 1) > min(len, npos) || __any(t.bad);
+    float zf[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) zf[i] = (float)((t.kz[i >> 2] >> (8 * (i & 3))) & 255u);
+    auto soft = [&](auto MASKED) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        uint32_t see = 0;
+        if constexpr (MASKED) {
+          see = t.bad ? 0u : seen(TP * tl + CH * g, tok[nb]);
+        }
+        float xs[CH], mx = NONE;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          xs[i] = (S[nb][i >> 2][i & 3] - zf[i] * qs0[nb]) * t.ks[i];
+          if constexpr (MASKED) xs[i] = (see >> i) & 1u ? xs[i] : NONE;
+          mx = fmaxf(mx, xs[i]);
+        }
+        const float Mn = fmaxf(M[nb], max_groups(mx));
+        const float ref = Mn * cq[nb];
+        if (__any(Mn > M[nb])) {
+          const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f(__builtin_fmaf(M[nb], cq[nb], -ref)) : 1.f;
+          l[nb] *= al;
+#pragma unroll
+          for (int i = 0; i < NO; ++i) acc[nb][i] *= al;
+        }
+        M[nb] = Mn;
+        float ps[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], cq[nb], -ref));
+          float f = e * t.vs[i];
+          if constexpr (MASKED) {
+            e = (see >> i) & 1u ? e : 0.f;
+            f = (see >> i) & 1u ? f : 0.f;
+          }
+          l[nb] += e;
+          ps[i] = f;
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
+            const float a = ps[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
+            const float b = ps[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
+            P[nb][0][s][j] = lead16(a, b);
+            P[nb][1][s][j] = lead16(rest16(a), rest16(b));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if (masked)
+      soft(std::integral_constant<bool, true>{});
+    else
+      soft(std::integral_constant<bool, false>{});
+  };
+  // zero points of the value operand's positions, in the form its codes have
+  uint32_t zl[2 * NI], zh[BITS == 4 ? 2 * NI : 1];
+  auto zeros = [&](const T& t) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      if constexpr (BITS == 8) {
+        zl[2 * j] = bytes2(t.vz[j], 0);
+        zl[2 * j + 1] = bytes2(t.vz[j], 1);
+      } else {
+        zl[2 * j] = nib_lo(t.vz[j]);
+        zl[2 * j + 1] = nib_lo(t.vz[j] >> 8);
+        zh[2 * j] = nib_hi(t.vz[j] << 4);
+        zh[2 * j + 1] = nib_hi(t.vz[j] >> 4);
+      }
+    }
+  };
+  auto values = [&](const T& t) {
+#pragma unroll
+    for (int i = 0; i < NMB; ++i) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        u32x4 a, e;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t u = t.v[i][2 * s + j];
+          const uint32_t *lo = zl + 4 * s + 2 * j, *hi = zh + (BITS == 4 ? 4 * s + 2 * j : 0);
+          if constexpr (BITS == 8) {
+            a[2 * j] = diff_bf16(bytes2(u, 0), lo[0]);
+            a[2 * j + 1] = diff_bf16(bytes2(u, 1), lo[1]);
+          } else {
+            a[2 * j] = diff_bf16(nib_lo(u), lo[0]);
+            a[2 * j + 1] = diff_bf16(nib_lo(u >> 8), lo[1]);
+            e[2 * j] = diff_bf16(nib_hi(u), hi[0]);
+            e[2 * j + 1] = diff_bf16(nib_hi(u >> 8), hi[1]);
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            acc[nb][i] = mfma_bf(a, P[nb][k][s], acc[nb][i]);
+            if constexpr (BITS == 4) acc[nb][i + NMB] = mfma_bf(e, P[nb][k][s], acc[nb][i + NMB]);
+          }
+        }
+      }
+      if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // A part of the next tile is asked for as soon as this tile's has been used.
+  if (tile < t1) {
+    T t;
+    Pages q = find(tile);
+    load_k(t, tile, q);
+    load_g(t, tile, q);
+    load_v(t, tile, q);
+    q = find(tile + 4);
+    while (true) {
+      const bool more = tile + 4 < t1;
+      scores(t);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_k(t, tile + 4, q);
+      __builtin_amdgcn_sched_barrier(0);
+      weights(t, tile);
+      zeros(t);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_g(t, tile + 4, q);
+      __builtin_amdgcn_sched_barrier(0);
+      values(t);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!more) break;
+      load_v(t, tile + 4, q);
+      tile += 4;
+      q = find(tile + 4);
+    }
+  }
+
+  // one row's sum from its four lanes
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    l[nb] = sum_groups(l[nb]);
+    M[nb] = M[nb] == NONE ? -INFINITY : M[nb] * cq[nb];
+    if constexpr (BITS == 4) {  // the upper half's codes came times 16
+#pragma unroll
+      for (int i = NMB; i < NO; ++i) acc[nb][i] *= 0.0625f;
+    }
+    if (g == 0) {
+      sm[w][16 * nb + n] = M[nb];
+      sl[w][16 * nb + n] = l[nb];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float mx = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, sm[k][16 * nb + n]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += sl[k][16 * nb + n] * __builtin_amdgcn_exp2f(sm[k][16 * nb + n] - ref);
+    const float f = __builtin_amdgcn_exp2f(M[nb] - ref);
+#pragma unroll
+    for (int i = 0; i < NO; ++i) acc[nb][i] *= f;
+    M[nb] = mx;
+    l[nb] = s;
+  }
+  auto put = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < NB * NO; ++i) so[k][i][lane] = acc[i / NO][i % NO];
+  };
+  auto add = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < NB * NO; ++i) acc[i / NO][i % NO] += so[k][i][lane];
+  };
+  if (w >= 2) put(w - 2);
+  __syncthreads();
+  if (w < 2) add(w);
+  __syncthreads();
+  if (w == 1) put(0);
+  __syncthreads();
+  if (w != 0) return;
+  add(0);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int rr = 16 * (NB * rb + nb) + n;
+    if (rr >= R) continue;
+    if (p.nsplit == 1) {
+      const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
+      uint16_t* o = p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        *(bf16x4*)(o + 16 * i + 4 * g) = __builtin_convertvector(acc[nb][i] * inv, bf16x4);
+      }
+    } else {
+      const size_t row = ((size_t)bh * R + rr) * p.nsplit + split;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) *(f32x4*)(p.part + row * DIM + 16 * i + 4 * g) = acc[nb][i];
+      if (g == 0) {
+        p.ml[2 * row] = M[nb];
+        p.ml[2 * row + 1] = l[nb];
+      }
+    }
   }
 }
 
+// Joins the shares of every row: sum of exp2(M_s - max M) (O_s, l_s), in order.
+__global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
+  const int q4 = p.c.dim >> 2, rows = 256 / q4;
+  const int i = threadIdx.x / q4, d = 4 * (threadIdx.x % q4);
+  const int R = p.tokens * p.group;
+  const long long row = (long long)blockIdx.x * rows + i;
+  if (i >= rows || row >= (long long)p.seqs * p.c.heads * R) return;
+  const float* ml = p.ml + 2 * row * p.nsplit;
+  float mx = -INFINITY, l = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  if (mx != -INFINITY)
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - mx);
+      l += f * ml[2 * s + 1];
+      a += f * *(const f32x4*)(p.part + (row * p.nsplit + s) * p.c.dim + d);
+    }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int bh = (int)(row / R), rr = (int)(row % R), b = bh / p.c.heads, h = bh % p.c.heads;
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  *(bf16x4*)(p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh + d) =
+      __builtin_convertvector(a * inv, bf16x4);
+}
+
+// Shares and row blocks of a call: 16 rows per block up to 16 rows, else 32,
+// else 64 (head sizes up to 128; the sums of larger ones do not fit).
+void plan_tree_attn(AttnProb& p, int ncu) {
+  const long long R = (long long)p.tokens * p.group;
+  p.nb = R <= 16 ? 1 : R <= 32 || p.c.dim > 128 ? 2 : 4;
+  p.nrb = (int)((R + 16 * p.nb - 1) / (16 * p.nb));
+  const long long items = (long long)p.seqs * p.c.heads * p.nrb;
+  const long long tiles = (((long long)p.width << p.c.pshift) + 63) / 64;
+  long long s = (2LL * ncu + items - 1) / items;
+  s = s < (tiles + 3) / 4 ? s : (tiles + 3) / 4;
+  p.nsplit = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+}
+
+namespace {
+template <int DIM, int BITS>
+void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
+  if (p.nb == 1)
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, DIM <= 128 ? 64 : 32, 2>), grid, dim3(256), 0, st, p);
+  else if (p.nb == 2)
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, DIM <= 128 ? 2 : 1>), grid, dim3(256), 0, st, p);
+  else if constexpr (DIM <= 128)
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 4, 32, 1>), grid, dim3(256), 0, st, p);
+}
+template <int BITS>
+hipError_t attn_dim(const AttnProb& p, hipStream_t st) {
+  const long long units = (long long)p.seqs * p.c.heads * p.nsplit;
+  const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.nrb));
+  switch (p.c.dim) {
+    case 64: attn_nb<64, BITS>(p, grid, st); break;
+    case 96: attn_nb<96, BITS>(p, grid, st); break;
+    case 128: attn_nb<128, BITS>(p, grid, st); break;
+    case 192: attn_nb<192, BITS>(p, grid, st); break;
+    default: attn_nb<256, BITS>(p, grid, st); break;
+  }
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st) {
-  const dim3 grid((unsigned)((long long)p.seqs * p.tokens * p.heads));
-  if (bits == 8)
-    hipLaunchKernelGGL(k_tree_attn<8>, grid, dim3(64), 0, st, p);
-  else
-    hipLaunchKernelGGL(k_tree_attn<4>, grid, dim3(64), 0, st, p);
+  return bits == 8 ? attn_dim<8>(p, st) : attn_dim<4>(p, st);
+}
+
+hipError_t launch_attn_join(const AttnProb& p, hipStream_t st) {
+  const int rows = 256 / (p.c.dim / 4);
+  const long long n = (long long)p.seqs * p.c.heads * p.tokens * p.group;
+  hipLaunchKernelGGL(k_attn_join, dim3((unsigned)((n + rows - 1) / rows)), dim3(256), 0, st, p);
   return hipGetLastError();
 }

@@ -62,6 +62,11 @@ struct AttnProb {
   int seqs, tokens, heads, group;  // group = heads / c.heads
   int width, words;
   float scale;  // of the scores, times log2(e)
+  // plan: row blocks of 16 nb rows, shares of the positions, and the shares'
+  // unnormalised rows [sequence][key head][row][share][dim] with their {M, l}
+  int nb, nrb, nsplit;
+  float* part;
+  float* ml;
 };
 
 hipError_t launch_rope_table(const RopeFreq& f, int length, int half, double mag, float* table, hipStream_t st);
@@ -69,4 +74,6 @@ hipError_t launch_rope_table(const RopeFreq& f, int length, int half, double mag
 hipError_t launch_rope(const RopeProb& p, int xtype, int ytype, int layout, hipStream_t st);
 hipError_t launch_kv_write(const KvWriteProb& p, int type, int bits, hipStream_t st);
 hipError_t launch_kv_read(const KvReadProb& p, int type, int bits, hipStream_t st);
+void plan_tree_attn(AttnProb& p, int ncu);
+hipError_t launch_attn_join(const AttnProb& p, hipStream_t st);
 hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st);
