@@ -23,6 +23,9 @@ __device__ __forceinline__ uint32_t bytes2(uint32_t w, int half) {
 __device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
 __device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w & 0x00F000F0u) | 0x64006400u; }
 
+__device__ __forceinline__ uint32_t sub16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) - __builtin_bit_cast(f16x2, b));
+}
 // float16 pair c minus float16 pair z as a bfloat16 pair (exact for integers up to 256)
 __device__ __forceinline__ uint32_t diff_bf16(uint32_t c, uint32_t z) {
   uint32_t lo, hi;
@@ -61,7 +64,6 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   const f32x2 v = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
-__device__ __forceinline__ float up16(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
 
 // One tile of TP positions as a lane holds it: see k_tree_attn.
 template <int DIM, int BITS, int TP>
@@ -74,11 +76,11 @@ struct Tile {
   static constexpr int NF = RB / 64;         // ... whole 64-byte pieces
   static constexpr bool R32 = RB % 64 >= 32, R16 = RB % 32 != 0;
   static constexpr int NMB = RB / 16;        // blocks of 16 byte rows of values
-  typedef uint32_t Chunk __attribute__((ext_vector_type(NI)));
+  typedef uint32_t Chunk __attribute__((ext_vector_type(NI)));  // a byte for each position of a chunk
   uint32_t k[NI][NW];
-  uint32_t v[NMB][NI];
-  float ks[CH], vs[CH];
-  uint32_t kz[NI], vz[NI];
+  Chunk v[NMB];
+  f32x4 ks[NI], vs[NI];
+  Chunk kz, vz;  // of the lane's key rows' chunk, of its own
   bool bad;
 
   // byte offset in a key row of word w of lane group g
@@ -103,12 +105,13 @@ struct Tile {
 //     the P^T operand as they are, and the V^T operand is as many consecutive
 //     bytes of a dimension's row, which is why values lie dimension by
 //     dimension in a page.  Every register of the sum belongs to row n.
-// Codes enter as 1024 + c (or 1024 + 16 c) in float16, made with one byte
-// permutation or mask for two codes.  The offset leaves the scores through
-// the MFMA's initial value -1024 sum q and z sum q.  Values enter as c - z in
-// bfloat16 (exact).  All products are exact in float32.
+// Codes enter as c - z: 1024 + c is made with one byte permutation or mask for
+// two codes, and 1024 + z taken from it; float16 in the first product, bfloat16
+// in the second, both exact, as all products are in float32.  Scores times
+// their position's scale are then relative to the row's factor cq.
 // Queries are scaled by a power of two per row to just below 2^15 (exact for
-// elements within 2^-29 of the largest) and exact in float16 (bf16 has 8 bits).
+// elements within 2^-29 of the largest) and exact in float16 (bf16 has 8 bits);
+// they wait in LDS in operand order.
 //
 // Weights enter the second product times their position's scale, as two
 // bfloat16 numbers, the leading 8 bits and the next 8: with one of them the
@@ -116,9 +119,9 @@ struct Tile {
 // would lose the weights under 2^-29 of the largest, which are all there is
 // where the others' values are zero.
 //
-// Positions of a tile after the context or on a page outside the pool go
-// through the masked form, which takes invisible positions out of maximum,
-// sum and weights by selection, whatever their scales hold.
+// In a tile that reaches past the context or a page outside the pool,
+// invisible positions are taken out of scores and weights by selection,
+// whatever their scales hold.
 //
 // The four waves of a workgroup take every fourth tile of its share of the
 // positions and are joined in LDS in a fixed order; with several shares
@@ -126,10 +129,14 @@ struct Tile {
 template <int DIM, int BITS, int NB, int TP, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   typedef Tile<DIM, BITS, TP> T;
+  typedef typename T::Chunk Chunk;
   constexpr int CH = T::CH, NI = T::NI, NS = T::NS;
   constexpr int NK = DIM / 32, NO = DIM / 16, NMB = T::NMB;
-  __shared__ float sm[4][16 * NB], sl[4][16 * NB];
-  __shared__ f32x4 so[2][NB * NO][64];
+  __shared__ float sm[4][16 * NB], sl[4][16 * NB], scq[16 * NB];
+  __shared__ union {
+    u32x4 q[NB][NK][64];
+    f32x4 o[2][NB * NO][64];
+  } sh;
   const KvPool& c = p.c;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -150,64 +157,6 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   const int t1 = min(ntile, (split + 1) * per);
   int tile = split * per + w;
 
-  // queries: row n of block nb
-  u32x4 qf[NB][NK];
-  float qs0[NB], qs1[NB], cq[NB];
-  int tok[NB];
-  const float asc = fabsf(p.scale);
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int rr = 16 * (NB * rb + nb) + n;
-    const int t = min(rr, R - 1) / p.group, hq = h * p.group + min(rr, R - 1) % p.group;
-    tok[nb] = t;
-    const uint16_t* q = p.q + b * p.qb + t * p.qt + hq * p.qh;
-    float v[NK][8];
-    float mx = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = BITS == 8 ? T::off(2 * ks + (e >> 2), g) + (e & 3) : 2 * T::off(ks, g) + (e >> 1) + 4 * (e & 1);
-        const float f = __uint_as_float((uint32_t)q[d] << 16);
-        v[ks][e] = rr < R ? f : 0.f;
-        mx = fmaxf(mx, fabsf(v[ks][e]));
-      }
-    }
-    mx = max_groups(mx);
-    const int ex = (int)(__float_as_uint(mx) >> 23);
-    const int sh = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^sh max in [2^14, 2^15)
-    const float up = __uint_as_float((uint32_t)(127 + sh) << 23), sgn = p.scale < 0.f ? -up : up;
-    cq[nb] = asc * __uint_as_float((uint32_t)(127 - sh) << 23);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // 4 bits: the odd codes of a word arrive times 16
-        const float f = BITS == 4 && (j & 1) ? sgn * 0.0625f : sgn;
-        o[j] = pack16(v[ks][2 * j] * f, v[ks][2 * j + 1] * f);
-        const float u = up16(o[j] & 0xFFFF) + up16(o[j] >> 16);
-        s1 += u;
-        s0 += BITS == 4 && (j & 1) ? 16.f * u : u;
-      }
-      qf[nb][ks] = u32x4{o[0], o[1], o[2], o[3]};
-    }
-    qs0[nb] = sum_groups(s0);
-    qs1[nb] = -1024.f * sum_groups(s1);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-
-  f32x4 acc[NB][NO];
-  float M[NB], l[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    M[nb] = NONE;
-    l[nb] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NO; ++i) acc[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
   const int pm = (1 << c.pshift) - 1, lastchunk = max(npos - 1, 0) / CH;
   const int* table = p.tables + (size_t)b * p.width;
   // page of a chunk (of the last one there is for those past the end)
@@ -216,21 +165,24 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
     bad = (unsigned)pg >= (unsigned)c.pages;
     return bad ? 0 : pg;
   };
-  // pages of the tile to be loaded next: of the lane's key rows, of its chunk
-  struct Pages {
-    int k, v;
-    bool bk, bv;
+  // (page, head) block and offset in it of the chunks of a tile that the lane
+  // reads: of its key rows, of its scores and values
+  struct Place {
+    int k, v, ok, ov;
+    bool bad;
   };
   auto find = [&](int tl) {
-    Pages q;
-    q.k = page_of(4 * tl + (n >> 2), q.bk);
-    q.v = page_of(4 * tl + g, q.bv);
+    Place q;
+    bool bk;
+    q.k = page_of(4 * tl + (n >> 2), bk);
+    q.v = page_of(4 * tl + g, q.bad);
+    q.ok = (min(4 * tl + (n >> 2), lastchunk) * CH) & pm;
+    q.ov = (min(4 * tl + g, lastchunk) * CH) & pm;
     return q;
   };
-  auto load_k = [&](T& t, int tl, const Pages& q) {
-    const size_t pk = (size_t)q.k * c.heads + h;
-    const int ok = (min(4 * tl + (n >> 2), lastchunk) * CH) & pm;
-    const uint8_t* kr = c.kc + ((pk << c.pshift) + ok + (n & 3)) * T::RB;
+  auto load_k = [&](T& t, const Place& q) {
+    const size_t at = (((size_t)q.k * c.heads + h) << c.pshift) + q.ok;
+    const uint8_t* kr = c.kc + (at + (n & 3)) * T::RB;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const uint8_t* r = kr + 4 * i * T::RB;
@@ -247,54 +199,113 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       }
       if constexpr (T::R16) t.k[i][T::NW - 1] = *glb((const uint32_t*)(r + T::RB - 16 + 4 * g));
     }
+    t.kz = *glb((const Chunk*)(c.kz + at));
   };
-  auto load_g = [&](T& t, int tl, const Pages& q) {
-    t.bad = q.bv;
-    const size_t at = (((size_t)q.v * c.heads + h) << c.pshift) + ((min(4 * tl + g, lastchunk) * CH) & pm);
+  auto load_g = [&](T& t, const Place& q) {
+    t.bad = q.bad;
+    const size_t at = (((size_t)q.v * c.heads + h) << c.pshift) + q.ov;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const f32x4 a = *glb((const f32x4*)(c.ks + at + 4 * i)), e = *glb((const f32x4*)(c.vs + at + 4 * i));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        t.ks[4 * i + r] = a[r];
-        t.vs[4 * i + r] = e[r];
-      }
+      t.ks[i] = *glb((const f32x4*)(c.ks + at + 4 * i));
+      t.vs[i] = *glb((const f32x4*)(c.vs + at + 4 * i));
     }
-    typedef typename T::Chunk Chunk;
-    const Chunk zk = *glb((const Chunk*)(c.kz + at)), zv = *glb((const Chunk*)(c.vz + at));
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      t.kz[i] = zk[i];
-      t.vz[i] = zv[i];
-    }
+    t.vz = *glb((const Chunk*)(c.vz + at));
   };
-  auto load_v = [&](T& t, int tl, const Pages& q) {
-    const size_t pv = (size_t)q.v * c.heads + h;
-    const uint8_t* vr = c.vc + ((pv * T::RB + n) << c.pshift) + ((min(4 * tl + g, lastchunk) * CH) & pm);
+  auto load_v = [&](T& t, const Place& q) {
+    const uint8_t* vr = c.vc + ((((size_t)q.v * c.heads + h) * T::RB + n) << c.pshift) + q.ov;
 #pragma unroll
-    for (int i = 0; i < NMB; ++i) {
-      typedef typename T::Chunk Chunk;
-      const Chunk u = *glb((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
-#pragma unroll
-      for (int e = 0; e < NI; ++e) t.v[i][e] = u[e];
-    }
+    for (int i = 0; i < NMB; ++i) t.v[i] = *glb((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
   };
 
-  // which of the positions j0 .. j0 + CH - 1 does drafted token t see
-  auto seen = [&](int j0, int t) -> uint32_t {
-    const int below = min(max(len - j0, 0), CH);
+  const bool work = tile < t1;
+  T t;
+  Place at{};
+  if (work) {
+    at = find(tile);
+    load_k(t, at);
+    load_g(t, at);
+    load_v(t, at);
+  }
+
+  // queries: row n of block nb, in the order of the key codes' words
+#pragma unroll 1
+  for (int nb = w; nb < NB; nb += 4) {
+    const int rr = 16 * (NB * rb + nb) + n, rc = min(rr, R - 1);
+    const uint16_t* q = p.q + b * p.qb + (rc / p.group) * p.qt + (h * p.group + rc % p.group) * p.qh;
+    float v[NK][8];
+    float mx = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      uint32_t u[4];
+      if constexpr (BITS == 8) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const u32x2 a = *glb((const u32x2*)(q + T::off(2 * ks + j, g)));
+          u[2 * j] = a[0];
+          u[2 * j + 1] = a[1];
+        }
+      } else {
+        const u32x4 a = *glb((const u32x4*)(q + 2 * T::off(ks, g)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = a[j];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // 4 bits: elements 0, 4, 1, 5, 2, 6, 3, 7 of the eight
+        const int i = BITS == 8 ? e : (e >> 1) + 4 * (e & 1);
+        const float f = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+        v[ks][e] = rr < R ? f : 0.f;
+        mx = fmaxf(mx, fabsf(v[ks][e]));
+      }
+    }
+    mx = max_groups(mx);
+    const int ex = (int)(__float_as_uint(mx) >> 23);
+    const int up = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^up mx in [2^14, 2^15)
+    float f = __uint_as_float((uint32_t)(127 + up) << 23);
+    if (p.scale < 0.f) f = -f;
+    if (p.scale == 0.f) f = 0.f;
+    // (a factor under 2^-100 leaves every weight at 1, as 2^-100 does)
+    if (g == 0) scq[16 * nb + n] = fmaxf(fabsf(p.scale) * __uint_as_float((uint32_t)(127 - up) << 23), 0x1p-100f);
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // 4 bits: the odd codes of a word arrive times 16
+        const float fj = BITS == 4 && (j & 1) ? f * 0.0625f : f;
+        o[j] = pack16(v[ks][2 * j] * fj, v[ks][2 * j + 1] * fj);
+      }
+      sh.q[nb][ks][lane] = o;
+    }
+  }
+  __syncthreads();
+
+  f32x4 acc[NB][NO];
+  float M[NB], l[NB], cq[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    M[nb] = NONE;
+    l[nb] = 0.f;
+    cq[nb] = scq[16 * nb + n];
+#pragma unroll
+    for (int i = 0; i < NO; ++i) acc[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // which of the positions j0 .. j0 + CH - 1 does the drafted token of row rr see
+  auto seen = [&](int j0, int rr) -> uint32_t {
+    const int below = min(max(len - j0, 0), CH), tk = min(rr, R - 1) / p.group;
     uint32_t bits;
     if (p.mask) {
       bits = 0;
       const int i0 = max(j0 - len, 0), wd = i0 >> 5;
-      const uint32_t* m = p.mask + ((size_t)b * p.tokens + t) * p.words;
+      const uint32_t* m = p.mask + ((size_t)b * p.tokens + tk) * p.words;
       if (below < CH) {
         const uint64_t lo = wd < p.words ? m[wd] : 0u, hi = wd + 1 < p.words ? m[wd + 1] : 0u;
         bits = (uint32_t)((hi << 32 | lo) >> (i0 & 31));
       }
       bits = bits << below | ((1u << below) - 1u);
     } else {
-      bits = (1u << min(max(len + t + 1 - j0, 0), CH)) - 1u;
+      bits = (1u << min(max(len + tk + 1 - j0, 0), CH)) - 1u;
     }
     return bits & ((1u << min(max(npos - j0, 0), CH)) - 1u);
   };
@@ -304,82 +315,75 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   auto scores = [&](const T& t) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
+      const uint32_t z = (t.kz[i] >> (8 * (n & 3))) & 255u;
+      const uint32_t zl = z * 0x00010001u + 0x64006400u, zh = z * 0x00100010u + 0x64006400u;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb][i] = f32x4{qs1[nb], qs1[nb], qs1[nb], qs1[nb]};
+      for (int nb = 0; nb < NB; ++nb) S[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
         u32x4 a;
         if constexpr (BITS == 8) {
           const uint32_t w0 = t.k[i][2 * ks], w1 = t.k[i][2 * ks + 1];
-          a = u32x4{bytes2(w0, 0), bytes2(w0, 1), bytes2(w1, 0), bytes2(w1, 1)};
+          a = u32x4{sub16(bytes2(w0, 0), zl), sub16(bytes2(w0, 1), zl), sub16(bytes2(w1, 0), zl),
+                    sub16(bytes2(w1, 1), zl)};
         } else {
           const uint32_t w0 = t.k[i][ks], w8 = w0 >> 8;
-          a = u32x4{nib_lo(w0), nib_hi(w0), nib_lo(w8), nib_hi(w8)};
+          a = u32x4{sub16(nib_lo(w0), zl), sub16(nib_hi(w0), zh), sub16(nib_lo(w8), zl), sub16(nib_hi(w8), zh)};
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, qf[nb][ks], S[nb][i]);
+        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, sh.q[nb][ks][lane], S[nb][i]);
       }
       if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
   auto weights = [&](const T& t, int tl) {
     const bool masked = TP * (tl + 1) > min(len, npos) || __any(t.bad);
-    float zf[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) zf[i] = (float)((t.kz[i >> 2] >> (8 * (i & 3))) & 255u);
-    auto soft = [&](auto MASKED) {
+    for (int nb = 0; nb < NB; ++nb) {
+      float xs[CH], mx = NONE;
+      uint32_t see = 0;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        uint32_t see = 0;
-        if constexpr (MASKED) {
-          see = t.bad ? 0u : seen(TP * tl + CH * g, tok[nb]);
-        }
-        float xs[CH], mx = NONE;
+      for (int i = 0; i < CH; ++i) xs[i] = S[nb][i >> 2][i & 3] * t.ks[i >> 2][i & 3];
+      if (masked) {
+        see = t.bad ? 0u : seen(TP * tl + CH * g, 16 * (NB * rb + nb) + n);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          xs[i] = (S[nb][i >> 2][i & 3] - zf[i] * qs0[nb]) * t.ks[i];
-          if constexpr (MASKED) xs[i] = (see >> i) & 1u ? xs[i] : NONE;
-          mx = fmaxf(mx, xs[i]);
-        }
-        const float Mn = fmaxf(M[nb], max_groups(mx));
-        const float ref = Mn * cq[nb];
-        if (__any(Mn > M[nb])) {
-          const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f(__builtin_fmaf(M[nb], cq[nb], -ref)) : 1.f;
-          l[nb] *= al;
-#pragma unroll
-          for (int i = 0; i < NO; ++i) acc[nb][i] *= al;
-        }
-        M[nb] = Mn;
-        float ps[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], cq[nb], -ref));
-          float f = e * t.vs[i];
-          if constexpr (MASKED) {
-            e = (see >> i) & 1u ? e : 0.f;
-            f = (see >> i) & 1u ? f : 0.f;
-          }
-          l[nb] += e;
-          ps[i] = f;
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
-            const float a = ps[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
-            const float b = ps[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
-            P[nb][0][s][j] = lead16(a, b);
-            P[nb][1][s][j] = lead16(rest16(a), rest16(b));
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : NONE;
       }
-    };
-    if (masked)
-      soft(std::integral_constant<bool, true>{});
-    else
-      soft(std::integral_constant<bool, false>{});
+#pragma unroll
+      for (int i = 0; i < CH; ++i) mx = fmaxf(mx, xs[i]);
+      const float Mn = fmaxf(M[nb], max_groups(mx));
+      // (nothing seen yet: NONE cq is far below every score's product with cq, and its weights are 0)
+      const float ref = Mn == NONE ? 0.f : Mn * cq[nb];
+      if (__any(Mn > M[nb])) {
+        const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f(__builtin_fmaf(M[nb], cq[nb], -ref)) : 1.f;
+        l[nb] *= al;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) acc[nb][i] *= al;
+      }
+      M[nb] = Mn;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], cq[nb], -ref));
+        l[nb] += e;
+        xs[i] = e * t.vs[i >> 2][i & 3];
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
+          const float a = xs[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
+          const float b = xs[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
+          P[nb][0][s][j] = lead16(a, b);
+          P[nb][1][s][j] = lead16(rest16(a), rest16(b));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   // zero points of the value operand's positions, in the form its codes have
   uint32_t zl[2 * NI], zh[BITS == 4 ? 2 * NI : 1];
@@ -431,30 +435,25 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   };
 
   // A part of the next tile is asked for as soon as this tile's has been used.
-  if (tile < t1) {
-    T t;
-    Pages q = find(tile);
-    load_k(t, tile, q);
-    load_g(t, tile, q);
-    load_v(t, tile, q);
-    q = find(tile + 4);
+  if (work) {
+    at = find(tile + 4);
     while (true) {
       const bool more = tile + 4 < t1;
       scores(t);
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_k(t, tile + 4, q);
+      if (more) load_k(t, at);
       __builtin_amdgcn_sched_barrier(0);
       weights(t, tile);
       zeros(t);
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_g(t, tile + 4, q);
+      if (more) load_g(t, at);
       __builtin_amdgcn_sched_barrier(0);
       values(t);
       __builtin_amdgcn_sched_barrier(0);
       if (!more) break;
-      load_v(t, tile + 4, q);
+      load_v(t, at);
       tile += 4;
-      q = find(tile + 4);
+      at = find(tile + 4);
     }
   }
 
@@ -489,11 +488,11 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   }
   auto put = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < NB * NO; ++i) so[k][i][lane] = acc[i / NO][i % NO];
+    for (int i = 0; i < NB * NO; ++i) sh.o[k][i][lane] = acc[i / NO][i % NO];
   };
   auto add = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < NB * NO; ++i) acc[i / NO][i % NO] += so[k][i][lane];
+    for (int i = 0; i < NB * NO; ++i) acc[i / NO][i % NO] += sh.o[k][i][lane];
   };
   if (w >= 2) put(w - 2);
   __syncthreads();
@@ -551,11 +550,10 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
       __builtin_convertvector(a * inv, bf16x4);
 }
 
-// Shares and row blocks of a call: 16 rows per block up to 16 rows, else 32,
-// else 64 (head sizes up to 128; the sums of larger ones do not fit).
+// Shares and row blocks of a call: 16 rows per block up to 16 rows, else 32.
 void plan_tree_attn(AttnProb& p, int ncu) {
   const long long R = (long long)p.tokens * p.group;
-  p.nb = R <= 16 ? 1 : R <= 32 || p.c.dim > 128 ? 2 : 4;
+  p.nb = R <= 16 ? 1 : 2;
   p.nrb = (int)((R + 16 * p.nb - 1) / (16 * p.nb));
   const long long items = (long long)p.seqs * p.c.heads * p.nrb;
   const long long tiles = (((long long)p.width << p.c.pshift) + 63) / 64;
@@ -569,10 +567,8 @@ template <int DIM, int BITS>
 void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
   if (p.nb == 1)
     hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, DIM <= 128 ? 64 : 32, 2>), grid, dim3(256), 0, st, p);
-  else if (p.nb == 2)
+  else
     hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, DIM <= 128 ? 2 : 1>), grid, dim3(256), 0, st, p);
-  else if constexpr (DIM <= 128)
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 4, 32, 1>), grid, dim3(256), 0, st, p);
 }
 template <int BITS>
 hipError_t attn_dim(const AttnProb& p, hipStream_t st) {
