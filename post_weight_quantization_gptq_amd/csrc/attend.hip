@@ -19,9 +19,16 @@ namespace {
 __device__ __forceinline__ uint32_t bytes2(uint32_t w, int half) {
   return __builtin_amdgcn_perm(0x64646464u, w, half ? 0x04030402u : 0x04010400u);
 }
-// the nibbles at bits 0 and 16 as 1024 + c, and those at bits 4 and 20 as 1024 + 16 c
-__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
-__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return (w & 0x00F000F0u) | 0x64006400u; }
+// the nibbles at bits 0 and 16 as 1024 + c, and those at bits 4 and 20 as 1024
+// + 16 c: one instruction each with both constants in registers (the compiler
+// takes two, with literals)
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(0x64006400u));
+  return r;
+}
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return and_or(w, 0x000F000Fu); }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return and_or(w, 0x00F000F0u); }
 
 __device__ __forceinline__ uint32_t sub16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) - __builtin_bit_cast(f16x2, b));
@@ -93,7 +100,8 @@ struct Tile {
 
 }  // namespace
 
-// Softmax attention in one pass over the cache with a running maximum and sum.
+// Softmax attention in one pass over the cache with a running reference near the
+// maximum and a running sum.
 //
 // A wave takes 16 NB query rows (token, head of the group) of one sequence and
 // key head, and TP = 64 or 32 positions at a time, and works with both products
@@ -351,16 +359,18 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       }
 #pragma unroll
       for (int i = 0; i < CH; ++i) mx = fmaxf(mx, xs[i]);
-      const float Mn = fmaxf(M[nb], max_groups(mx));
-      // (nothing seen yet: NONE cq is far below every score's product with cq, and its weights are 0)
-      const float ref = Mn == NONE ? 0.f : Mn * cq[nb];
-      if (__any(Mn > M[nb])) {
-        const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f(__builtin_fmaf(M[nb], cq[nb], -ref)) : 1.f;
+      // M moves only when a score passes it by 2^8 (its weight): most tiles then
+      // need neither the maximum over the lanes nor a pass over the sums.
+      if (__any((mx - M[nb]) * cq[nb] > 8.f)) {
+        const float Mn = fmaxf(M[nb], max_groups(mx));
+        const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f((M[nb] - Mn) * cq[nb]) : 1.f;
         l[nb] *= al;
 #pragma unroll
         for (int i = 0; i < NO; ++i) acc[nb][i] *= al;
+        M[nb] = Mn;
       }
-      M[nb] = Mn;
+      // (nothing seen yet: NONE cq is far below every score's product with cq, and its weights are 0)
+      const float ref = M[nb] == NONE ? 0.f : M[nb] * cq[nb];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], cq[nb], -ref));
@@ -526,23 +536,44 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   }
 }
 
-// Joins the shares of every row: sum of exp2(M_s - max M) (O_s, l_s), in order.
+// Joins the shares of every row: sum of exp2(M_s - max M) (O_s, l_s).  G
+// threads of a row take every G-th share of four dimensions each, and are added
+// in order.
+template <int G>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
-  const int q4 = p.c.dim >> 2, rows = 256 / q4;
-  const int i = threadIdx.x / q4, d = 4 * (threadIdx.x % q4);
+  __shared__ f32x4 so[256];
+  __shared__ float sl[256];
+  const int q4 = p.c.dim >> 2, rows = 256 / (q4 * G);
+  const int i = threadIdx.x / (q4 * G), k = threadIdx.x / q4 % G, d = 4 * (threadIdx.x % q4);
   const int R = p.tokens * p.group;
   const long long row = (long long)blockIdx.x * rows + i;
-  if (i >= rows || row >= (long long)p.seqs * p.c.heads * R) return;
-  const float* ml = p.ml + 2 * row * p.nsplit;
-  float mx = -INFINITY, l = 0.f;
-  for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+  const bool on = i < rows && row < (long long)p.seqs * p.c.heads * R;
   f32x4 a = {0.f, 0.f, 0.f, 0.f};
-  if (mx != -INFINITY)
-    for (int s = 0; s < p.nsplit; ++s) {
-      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - mx);
-      l += f * ml[2 * s + 1];
-      a += f * *(const f32x4*)(p.part + (row * p.nsplit + s) * p.c.dim + d);
+  float l = 0.f;
+  if (on) {
+    const float* ml = p.ml + 2 * row * p.nsplit;
+    float mx = -INFINITY;
+    for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+    if (mx != -INFINITY) {
+#pragma unroll 4
+      for (int s = k; s < p.nsplit; s += G) {
+        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - mx);
+        l += f * ml[2 * s + 1];
+        a += f * *(const f32x4*)(p.part + (row * p.nsplit + s) * p.c.dim + d);
+      }
     }
+  }
+  if (G > 1) {
+    so[threadIdx.x] = a;
+    sl[threadIdx.x] = l;
+    __syncthreads();
+    if (k != 0) return;
+    for (int e = 1; e < G; ++e) {
+      a += so[threadIdx.x + e * q4];
+      l += sl[threadIdx.x + e * q4];
+    }
+  }
+  if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int bh = (int)(row / R), rr = (int)(row % R), b = bh / p.c.heads, h = bh % p.c.heads;
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -550,11 +581,13 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
       __builtin_convertvector(a * inv, bf16x4);
 }
 
-// Shares and row blocks of a call: 16 rows per block up to 16 rows, else 32.
+// Shares and row blocks of a call: as few blocks as blocks of up to 48 rows
+// (32 for head sizes above 128, whose sums need the registers) allow, of equal size.
 void plan_tree_attn(AttnProb& p, int ncu) {
   const long long R = (long long)p.tokens * p.group;
-  p.nb = R <= 16 ? 1 : 2;
-  p.nrb = (int)((R + 16 * p.nb - 1) / (16 * p.nb));
+  const long long r16 = (R + 15) / 16, most = p.c.dim <= 128 ? 3 : 2;
+  p.nrb = (int)((r16 + most - 1) / most);
+  p.nb = (int)((r16 + p.nrb - 1) / p.nrb);
   const long long items = (long long)p.seqs * p.c.heads * p.nrb;
   const long long tiles = (((long long)p.width << p.c.pshift) + 63) / 64;
   long long s = (2LL * ncu + items - 1) / items;
@@ -567,8 +600,10 @@ template <int DIM, int BITS>
 void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
   if (p.nb == 1)
     hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, DIM <= 128 ? 64 : 32, 2>), grid, dim3(256), 0, st, p);
-  else
+  else if (p.nb == 2)
     hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, DIM <= 128 ? 2 : 1>), grid, dim3(256), 0, st, p);
+  else if constexpr (DIM <= 128)
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 3, 32, 2>), grid, dim3(256), 0, st, p);
 }
 template <int BITS>
 hipError_t attn_dim(const AttnProb& p, hipStream_t st) {
@@ -590,8 +625,12 @@ hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st) {
 }
 
 hipError_t launch_attn_join(const AttnProb& p, hipStream_t st) {
-  const int rows = 256 / (p.c.dim / 4);
+  const int G = p.nsplit >= 8 ? 4 : 1, rows = 256 / (p.c.dim / 4 * G);
   const long long n = (long long)p.seqs * p.c.heads * p.tokens * p.group;
-  hipLaunchKernelGGL(k_attn_join, dim3((unsigned)((n + rows - 1) / rows)), dim3(256), 0, st, p);
+  const dim3 grid((unsigned)((n + rows - 1) / rows));
+  if (G == 4)
+    hipLaunchKernelGGL(k_attn_join<4>, grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL(k_attn_join<1>, grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
