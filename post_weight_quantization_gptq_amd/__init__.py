@@ -212,6 +212,7 @@ class KVCache:
             setattr(self, name, t)
         self.bits, self.pages, self.heads, self.page, self.dim = bits, pages, heads, page, rb * 8 // bits
         self.device = k_codes.device
+        self._index = self.device.index
         self._c = _KV(*[t.data_ptr() for t in given], pages, heads, page, self.dim, bits, 0)
 
 
@@ -227,6 +228,8 @@ class Context:
             raise ValueError("the GPTQ library needs a GPU device")
         self.device = torch.device("cuda", dev.index if dev.index is not None else torch.cuda.current_device())
         self.stream = torch.cuda.current_stream(self.device)
+        self._raw = self.stream.cuda_stream
+        self._current_raw = torch._C._cuda_getCurrentRawStream
         h = ctypes.c_void_p()
         self._check(self.lib.gptq_create(ctypes.byref(h), self.device.index, ctypes.c_void_p(self.stream.cuda_stream)),
                     ctx=None)
@@ -601,24 +604,37 @@ class Context:
         return Y
 
     # ------------------------------------------------------ serving operators
-    def _here(self, tensors, cache=None):
-        """With another torch stream current than the context's, tell the allocator that the
-        call's tensors are used on the context's stream."""
-        torch = self.torch
-        if torch.cuda.current_stream(self.device).cuda_stream != self.stream.cuda_stream:
-            if cache is not None:
-                tensors += tuple(getattr(cache, name) for name in KVCache.FIELDS)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+    # (called once per layer and token: their checks are kept to a few attribute reads)
+    def _elsewhere(self):
+        """Whether another torch stream is current than the context's."""
+        return self._current_raw(self.device.index) != self._raw
 
-    def _empty(self, shape, dtype):
+    def _here(self, tensors, cache=None):
+        """With another torch stream current, tell the allocator that the call's tensors are
+        used on the context's stream."""
+        if cache is not None:
+            tensors += tuple(getattr(cache, name) for name in KVCache.FIELDS)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(self.stream)
+
+    def _empty(self, shape, dtype, elsewhere=None):
         """An output tensor whose memory belongs to the context's stream."""
         torch = self.torch
-        if torch.cuda.current_stream(self.device).cuda_stream == self.stream.cuda_stream:
+        if not (self._elsewhere() if elsewhere is None else elsewhere):
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _plain(self, t, dtype, shape, name):
+        """t as a contiguous tensor of the given type and shape on the context's device."""
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.get_device() != self.device.index or not t.is_contiguous():
+            raise ValueError("%s must be contiguous on %s" % (name, self.device))
+        if t.shape != shape:
+            raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+        return t.data_ptr()
 
     def _type(self, dtype, name):
         torch = self.torch
@@ -630,16 +646,17 @@ class Context:
 
     def _rows(self, t, ndim, name):
         """t as rows [..., heads, dim] with the last dimension contiguous."""
-        if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        st = t.stride()
+        if len(st) != ndim or (st[-1] != 1 and t.shape[-1] > 1):
             raise ValueError("%s must have %d dimensions, the last of them contiguous" % (name, ndim))
-        if t.device != self.device:
+        if t.get_device() != self.device.index:
             raise ValueError("%s must be on %s" % (name, self.device))
-        return t
+        return st
 
     def _cache(self, cache):
         if not isinstance(cache, KVCache):
             raise TypeError("cache must be a KVCache")
-        if cache.device != self.device:
+        if cache._index != self.device.index:
             raise ValueError("the cache must be on %s" % self.device)
         return ctypes.byref(cache._c)
 
@@ -678,63 +695,66 @@ class Context:
         rope_table; the first 2 * table.shape[2] values of a head are turned, the rest copied.  `out` may be
         x itself; otherwise a new tensor of out_dtype (default: x's)."""
         torch = self.torch
-        x = self._rows(x, 3, "x")
+        xs = self._rows(x, 3, "x")
         tokens, heads, dim = x.shape
         if layout not in _ROPE_LAYOUTS:
             raise ValueError("layout must be 'half' or 'interleaved'")
-        self._dev(table, torch.float32, "table")
-        self._dev(positions, torch.int32, "positions")
         if table.dim() != 3 or table.shape[1] != 2 or 2 * table.shape[2] > dim:
             raise ValueError("table must be [length, 2, rot/2] with rot at most the head size")
-        if positions.shape != (tokens,):
-            raise ValueError("positions must hold one entry per token")
+        tp = self._plain(table, torch.float32, table.shape, "table")
+        pp = self._plain(positions, torch.int32, (tokens,), "positions")
+        away = self._elsewhere()
         if out is None:
-            out = self._empty((tokens, heads, dim), x.dtype if out_dtype is None else out_dtype)
+            out = self._empty((tokens, heads, dim), x.dtype if out_dtype is None else out_dtype, away)
         elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError("out must have x's shape and the output type")
-        self._rows(out, 3, "out")
-        self._here((x, positions, table, out))
+        ys = self._rows(out, 3, "out")
+        if away:
+            self._here((x, positions, table, out))
+        length, _, half = table.shape
         self._check(self.lib.gptq_rope(
-            self.handle, x.data_ptr(), self._type(x.dtype, "x"), tokens, heads, dim, x.stride(0), x.stride(1),
-            positions.data_ptr(), table.data_ptr(), table.shape[0], 2 * table.shape[2], _ROPE_LAYOUTS[layout],
-            int(bool(inverse)), out.data_ptr(), self._type(out.dtype, "out"), out.stride(0), out.stride(1)))
+            self.handle, x.data_ptr(), self._type(x.dtype, "x"), tokens, heads, dim, xs[0], xs[1], pp, tp, length,
+            2 * half, _ROPE_LAYOUTS[layout], 1 if inverse else 0, out.data_ptr(), self._type(out.dtype, "out"), ys[0],
+            ys[1]))
         return out
 
     def kv_write(self, cache, k, v, slots):
         """Quantise k and v [tokens, heads, dim] (both bf16 or both fp32) into the cache at `slots` (int32,
         page * cache.page + offset; negative: skipped)."""
         c = self._cache(cache)
-        k, v = self._rows(k, 3, "k"), self._rows(v, 3, "v")
+        ks, vs = self._rows(k, 3, "k"), self._rows(v, 3, "v")
         tokens = k.shape[0]
         if k.shape != (tokens, cache.heads, cache.dim) or v.shape != k.shape:
             raise ValueError("k and v must be [tokens, %d, %d]" % (cache.heads, cache.dim))
-        if v.dtype != k.dtype:
+        if v.dtype is not k.dtype:
             raise TypeError("k and v must have the same type")
-        self._dev(slots, self.torch.int32, "slots")
-        if slots.shape != (tokens,):
-            raise ValueError("slots must hold one entry per token")
-        self._here((k, v, slots), cache)
+        sp = self._plain(slots, self.torch.int32, (tokens,), "slots")
+        if self._elsewhere():
+            self._here((k, v, slots), cache)
         self._check(self.lib.gptq_kv_write(self.handle, c, k.data_ptr(), v.data_ptr(), self._type(k.dtype, "k"), tokens,
-                                           k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr()))
+                                           ks[0], ks[1], vs[0], vs[1], sp))
 
     def kv_read(self, cache, slots, dtype=None, k=None, v=None):
         """(k, v) [tokens, heads, dim] of the tokens at `slots`, as bf16 (default) or fp32; zeros for slots
         outside the pool."""
         torch = self.torch
         c = self._cache(cache)
-        self._dev(slots, torch.int32, "slots")
         if slots.dim() != 1:
             raise ValueError("slots must have one dimension")
+        sp = self._plain(slots, torch.int32, slots.shape, "slots")
         shape = (slots.shape[0], cache.heads, cache.dim)
         dtype = dtype if dtype is not None else k.dtype if k is not None else torch.bfloat16
         kind = self._type(dtype, "dtype")
-        k = self._empty(shape, dtype) if k is None else self._rows(k, 3, "k")
-        v = self._empty(shape, dtype) if v is None else self._rows(v, 3, "v")
-        if k.shape != shape or v.shape != shape or k.dtype != dtype or v.dtype != dtype:
+        away = self._elsewhere()
+        k = self._empty(shape, dtype, away) if k is None else k
+        v = self._empty(shape, dtype, away) if v is None else v
+        ks, vs = self._rows(k, 3, "k"), self._rows(v, 3, "v")
+        if k.shape != shape or v.shape != shape or k.dtype is not dtype or v.dtype is not dtype:
             raise ValueError("k and v must be %s of %s" % (list(shape), dtype))
-        self._here((slots, k, v), cache)
-        self._check(self.lib.gptq_kv_read(self.handle, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), kind,
-                                          k.stride(0), k.stride(1), v.stride(0), v.stride(1)))
+        if away:
+            self._here((slots, k, v), cache)
+        self._check(self.lib.gptq_kv_read(self.handle, c, sp, shape[0], k.data_ptr(), v.data_ptr(), kind, ks[0], ks[1],
+                                          vs[0], vs[1]))
         return k, v
 
     def tree_attention(self, q, cache, tables, lengths, mask=None, scale: float | None = None, out=None):
@@ -745,35 +765,36 @@ class Context:
         drafted token t sees drafted token i (None: a chain).  scale defaults to dim ** -0.5.  bf16 result."""
         torch = self.torch
         c = self._cache(cache)
-        q = self._rows(q, 4, "q")
+        qs = self._rows(q, 4, "q")
         seqs, tokens, heads, dim = q.shape
         if q.dtype is not torch.bfloat16:
             raise TypeError("q must be bfloat16")
         if dim != cache.dim or heads % cache.heads:
             raise ValueError("q must have heads a multiple of %d and dim %d" % (cache.heads, cache.dim))
-        self._dev(tables, torch.int32, "tables")
-        self._dev(lengths, torch.int32, "lengths")
-        if tables.dim() != 2 or tables.shape[0] != seqs or lengths.shape != (seqs,):
-            raise ValueError("tables must be [seqs, width] and lengths [seqs]")
-        words = 0
+        if tables.dim() != 2:
+            raise ValueError("tables must be [seqs, width]")
+        width = tables.shape[1]
+        tp = self._plain(tables, torch.int32, (seqs, width), "tables")
+        lp = self._plain(lengths, torch.int32, (seqs,), "lengths")
+        words, mp = 0, None
         if mask is not None:
-            self._dev(mask, torch.int32, "mask")
-            if mask.dim() != 3 or mask.shape[0] != seqs or mask.shape[1] != tokens:
+            if mask.dim() != 3:
                 raise ValueError("mask must be [seqs, tokens, words]")
             words = mask.shape[2]
+            mp = self._plain(mask, torch.int32, (seqs, tokens, words), "mask")
             if 32 * words < tokens:  # (an empty tensor's null pointer would mean a chain)
                 raise GPTQError(1, "a mask row has too few words")
+        away = self._elsewhere()
         if out is None:
-            out = self._empty(q.shape, torch.bfloat16)
+            out = self._empty(q.shape, torch.bfloat16, away)
         elif out.shape != q.shape or out.dtype is not torch.bfloat16:
             raise ValueError("out must be bfloat16 of q's shape")
-        self._rows(out, 4, "out")
-        self._here((q, tables, lengths, mask, out), cache)
+        os_ = self._rows(out, 4, "out")
+        if away:
+            self._here((q, tables, lengths, mask, out), cache)
         self._check(self.lib.gptq_tree_attention(
-            self.handle, c, q.data_ptr(), seqs, tokens, heads, q.stride(0), q.stride(1), q.stride(2),
-            tables.data_ptr(), tables.shape[1], lengths.data_ptr(), mask.data_ptr() if mask is not None else None, words,
-            dim ** -0.5 if scale is None else float(scale), out.data_ptr(), out.stride(0), out.stride(1),
-            out.stride(2)))
+            self.handle, c, q.data_ptr(), seqs, tokens, heads, qs[0], qs[1], qs[2], tp, width, lp, mp, words,
+            dim ** -0.5 if scale is None else float(scale), out.data_ptr(), os_[0], os_[1], os_[2]))
         return out
 
     def quantize_batched(self, layers):

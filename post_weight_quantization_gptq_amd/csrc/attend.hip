@@ -2,7 +2,7 @@
 #include "common.h"
 #include "serve.h"
 
-#include <type_traits>
+#include <algorithm>
 
 // running maximum of a row that has seen nothing (finite: its product with a zero scale is 0)
 #define NONE (-3.402823466e38f)
@@ -11,6 +11,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 namespace {
 
@@ -98,6 +99,67 @@ struct Tile {
   }
 };
 
+// Rows that another workgroup of the same launch reads, perhaps on another
+// XCD: stored through and loaded past the L2 (agent-scope accesses), so that no
+// cache has to be written back or emptied for them.  (A fence pair, which does
+// that, took 90 us of a 180 us call.)
+__device__ __forceinline__ void put_shared(float* p, float a, float b) {
+  const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <bool SHARED>
+__device__ __forceinline__ f32x2 get2(const float* p) {
+  if (!SHARED) return *(const f32x2*)p;
+  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return f32x2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
+}
+
+// Joins the shares of row `row` of (sequence, key head, row), dimensions d .. d
+// + 3: sum of exp2(M_s - max M) (O_s, l_s).  G threads take every G-th share
+// each (k says which) and are added in order; row < 0: takes part only.
+template <int G>
+struct JoinLds {
+  f32x4 o[G > 1 ? 256 : 1];
+  float l[G > 1 ? 256 : 1];
+};
+template <int G, bool SHARED>
+__device__ __forceinline__ void join_row(const AttnProb& p, long long row, int d, int k, JoinLds<G>* s) {
+  const int dim = p.c.dim, ns = p.nsplit;
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  if (row >= 0) {
+    const float* ml = p.ml + 2 * row * ns;
+    float mx = -INFINITY;
+#pragma unroll 8
+    for (int e = 0; e < ns; ++e) mx = fmaxf(mx, get2<SHARED>(ml + 2 * e)[0]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float* part = p.part + row * ns * dim + d;
+#pragma unroll 4
+    for (int e = k; e < ns; e += G) {
+      const f32x2 o0 = get2<SHARED>(part + (size_t)e * dim), o1 = get2<SHARED>(part + (size_t)e * dim + 2);
+      const f32x2 m = get2<SHARED>(ml + 2 * e);
+      const float f = __builtin_amdgcn_exp2f(m[0] - ref);
+      l += f * m[1];
+      a += f * f32x4{o0[0], o0[1], o1[0], o1[1]};
+    }
+  }
+  if constexpr (G > 1) {
+    s->o[threadIdx.x] = a;
+    s->l[threadIdx.x] = l;
+    __syncthreads();
+    if (k != 0) return;
+    for (int e = 1; e < G; ++e) {
+      a += s->o[threadIdx.x + e * (dim >> 2)];
+      l += s->l[threadIdx.x + e * (dim >> 2)];
+    }
+  }
+  if (row < 0) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int R = p.tokens * p.group, bh = (int)(row / R), rr = (int)(row % R), b = bh / p.c.heads, h = bh % p.c.heads;
+  *(bf16x4*)(p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh + d) =
+      __builtin_convertvector(a * inv, bf16x4);
+}
+
 }  // namespace
 
 // Softmax attention in one pass over the cache with a running reference near the
@@ -133,7 +195,9 @@ struct Tile {
 //
 // The four waves of a workgroup take every fourth tile of its share of the
 // positions and are joined in LDS in a fixed order; with several shares
-// (nsplit) the unnormalised rows go to the workspace for k_attn_join.
+// (nsplit) the unnormalised rows go to the workspace.  The shares of a row are
+// joined, in their order, by the workgroup that comes last (p.count, which it
+// sets back to 0), or where they are many by k_attn_join.
 template <int DIM, int BITS, int NB, int TP, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   typedef Tile<DIM, BITS, TP> T;
@@ -321,27 +385,35 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   f32x4 S[NB][NI];
   u32x4 P[NB][2][NS];  // [leading, next][step]
   auto scores = [&](const T& t) {
+    uint32_t zl[NI], zh[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const uint32_t z = (t.kz[i] >> (8 * (n & 3))) & 255u;
-      const uint32_t zl = z * 0x00010001u + 0x64006400u, zh = z * 0x00100010u + 0x64006400u;
+      zl[i] = z * 0x00010001u + 0x64006400u;
+      zh[i] = z * 0x00100010u + 0x64006400u;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) S[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
+    for (int ks = 0; ks < NK; ++ks) {
+      u32x4 q[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) q[nb] = sh.q[nb][ks][lane];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
         u32x4 a;
         if constexpr (BITS == 8) {
           const uint32_t w0 = t.k[i][2 * ks], w1 = t.k[i][2 * ks + 1];
-          a = u32x4{sub16(bytes2(w0, 0), zl), sub16(bytes2(w0, 1), zl), sub16(bytes2(w1, 0), zl),
-                    sub16(bytes2(w1, 1), zl)};
+          a = u32x4{sub16(bytes2(w0, 0), zl[i]), sub16(bytes2(w0, 1), zl[i]), sub16(bytes2(w1, 0), zl[i]),
+                    sub16(bytes2(w1, 1), zl[i])};
         } else {
           const uint32_t w0 = t.k[i][ks], w8 = w0 >> 8;
-          a = u32x4{sub16(nib_lo(w0), zl), sub16(nib_hi(w0), zh), sub16(nib_lo(w8), zl), sub16(nib_hi(w8), zh)};
+          a = u32x4{sub16(nib_lo(w0), zl[i]), sub16(nib_hi(w0), zh[i]), sub16(nib_lo(w8), zl[i]),
+                    sub16(nib_hi(w8), zh[i])};
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, sh.q[nb][ks][lane], S[nb][i]);
+        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, q[nb], S[nb][i]);
       }
-      if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
   auto weights = [&](const T& t, int tl) {
@@ -411,6 +483,8 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       }
     }
   };
+  // vector instructions a product: what unpacking takes, over the products
+  constexpr int VPM = NB == 1 ? 8 : NB == 2 ? 4 : 3;
   auto values = [&](const T& t) {
 #pragma unroll
     for (int i = 0; i < NMB; ++i) {
@@ -432,15 +506,21 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
           }
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int nb = 0; nb < NB; ++nb) {
             acc[nb][i] = mfma_bf(a, P[nb][k][s], acc[nb][i]);
             if constexpr (BITS == 4) acc[nb][i + NMB] = mfma_bf(e, P[nb][k][s], acc[nb][i + NMB]);
           }
         }
       }
-      if constexpr (NB > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    // the next codes are unpacked between the products: a product keeps its
+    // unit busy for four further instructions' time
+#pragma unroll
+    for (int i = 0; i < 2 * NB * NO * NS; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x002, VPM, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     }
   };
 
@@ -510,75 +590,55 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   __syncthreads();
   if (w == 1) put(0);
   __syncthreads();
-  if (w != 0) return;
-  add(0);
+  if (w == 0) {
+    add(0);
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int rr = 16 * (NB * rb + nb) + n;
-    if (rr >= R) continue;
-    if (p.nsplit == 1) {
-      const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
-      uint16_t* o = p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int rr = 16 * (NB * rb + nb) + n;
+      if (rr >= R) continue;
+      if (p.nsplit == 1) {
+        const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
+        uint16_t* o = p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh;
 #pragma unroll
-      for (int i = 0; i < NO; ++i) {
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        *(bf16x4*)(o + 16 * i + 4 * g) = __builtin_convertvector(acc[nb][i] * inv, bf16x4);
-      }
-    } else {
-      const size_t row = ((size_t)bh * R + rr) * p.nsplit + split;
+        for (int i = 0; i < NO; ++i)
+          *(bf16x4*)(o + 16 * i + 4 * g) = __builtin_convertvector(acc[nb][i] * inv, bf16x4);
+      } else {
+        const size_t row = ((size_t)bh * R + rr) * p.nsplit + split;
 #pragma unroll
-      for (int i = 0; i < NO; ++i) *(f32x4*)(p.part + row * DIM + 16 * i + 4 * g) = acc[nb][i];
-      if (g == 0) {
-        p.ml[2 * row] = M[nb];
-        p.ml[2 * row + 1] = l[nb];
+        for (int i = 0; i < NO; ++i) {
+          float* o = p.part + row * DIM + 16 * i + 4 * g;
+          put_shared(o, acc[nb][i][0], acc[nb][i][1]);
+          put_shared(o + 2, acc[nb][i][2], acc[nb][i][3]);
+        }
+        if (g == 0) put_shared(p.ml + 2 * row, M[nb], l[nb]);
       }
     }
   }
+  if (!p.count) return;
+  __shared__ int last;
+  if (w == 0) {
+    // this wave wrote the rows: they are in memory before the count says so
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (lane == 0) {
+      int* ct = p.count + (size_t)bh * p.nrb + rb;
+      last = __hip_atomic_fetch_add(ct, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.nsplit - 1;
+      if (last) __hip_atomic_store(ct, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  const int r1 = min(16 * NB, R - 16 * NB * rb);
+  for (int i = tid; i < r1 * (DIM / 4); i += 256)
+    join_row<1, true>(p, (long long)bh * R + 16 * NB * rb + i / (DIM / 4), 4 * (i % (DIM / 4)), 0, nullptr);
 }
 
-// Joins the shares of every row: sum of exp2(M_s - max M) (O_s, l_s).  G
-// threads of a row take every G-th share of four dimensions each, and are added
-// in order.
 template <int G>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
-  __shared__ f32x4 so[256];
-  __shared__ float sl[256];
-  const int q4 = p.c.dim >> 2, rows = 256 / (q4 * G);
+  __shared__ JoinLds<G> s;
+  const int q4 = p.c.dim >> 2, rows = max(256 / (q4 * G), 1);
   const int i = threadIdx.x / (q4 * G), k = threadIdx.x / q4 % G, d = 4 * (threadIdx.x % q4);
-  const int R = p.tokens * p.group;
   const long long row = (long long)blockIdx.x * rows + i;
-  const bool on = i < rows && row < (long long)p.seqs * p.c.heads * R;
-  f32x4 a = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  if (on) {
-    const float* ml = p.ml + 2 * row * p.nsplit;
-    float mx = -INFINITY;
-    for (int s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
-    if (mx != -INFINITY) {
-#pragma unroll 4
-      for (int s = k; s < p.nsplit; s += G) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - mx);
-        l += f * ml[2 * s + 1];
-        a += f * *(const f32x4*)(p.part + (row * p.nsplit + s) * p.c.dim + d);
-      }
-    }
-  }
-  if (G > 1) {
-    so[threadIdx.x] = a;
-    sl[threadIdx.x] = l;
-    __syncthreads();
-    if (k != 0) return;
-    for (int e = 1; e < G; ++e) {
-      a += so[threadIdx.x + e * q4];
-      l += sl[threadIdx.x + e * q4];
-    }
-  }
-  if (!on) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int bh = (int)(row / R), rr = (int)(row % R), b = bh / p.c.heads, h = bh % p.c.heads;
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  *(bf16x4*)(p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh + d) =
-      __builtin_convertvector(a * inv, bf16x4);
+  join_row<G, false>(p, i < rows && row < (long long)p.seqs * p.c.heads * p.tokens * p.group ? row : -1, d, k, &s);
 }
 
 // Shares and row blocks of a call: as few blocks as blocks of up to 48 rows
@@ -625,10 +685,15 @@ hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st) {
 }
 
 hipError_t launch_attn_join(const AttnProb& p, hipStream_t st) {
-  const int G = p.nsplit >= 8 ? 4 : 1, rows = 256 / (p.c.dim / 4 * G);
+  // eight threads for a value where there are many shares: 160 rows of 128
+  // shares 8 us, 15 with one; 13824 rows of three shares 5 us, 11 with eight
+  const int G = p.nsplit >= 16 && p.c.dim <= 128 ? 8 : p.nsplit >= 16 ? 4 : 1;
+  const int rows = std::max(256 / (p.c.dim / 4 * G), 1);
   const long long n = (long long)p.seqs * p.c.heads * p.tokens * p.group;
   const dim3 grid((unsigned)((n + rows - 1) / rows));
-  if (G == 4)
+  if (G == 8)
+    hipLaunchKernelGGL(k_attn_join<8>, grid, dim3(256), 0, st, p);
+  else if (G == 4)
     hipLaunchKernelGGL(k_attn_join<4>, grid, dim3(256), 0, st, p);
   else
     hipLaunchKernelGGL(k_attn_join<1>, grid, dim3(256), 0, st, p);

@@ -67,6 +67,7 @@ struct AttnProb {
   int nb, nrb, nsplit;
   float* part;
   float* ml;
+  int* count;  // one for each row block of a (sequence, key head), 0 between calls; null: k_attn_join follows
 };
 
 hipError_t launch_rope_table(const RopeFreq& f, int length, int half, double mag, float* table, hipStream_t st);
