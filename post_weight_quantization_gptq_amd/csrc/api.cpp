@@ -1440,7 +1440,8 @@ GPTQ_API int gptq_kv_write(gptq_ctx c, const gptq_kv_cache* cache, const void* K
   if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
   if (tokens == 0) return GPTQ_OK;
   if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens > INT32_MAX || (tokens + 63) / 64 * cache->heads > (1 << 28))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
   if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
   if (cache->heads == 1) k_head = v_head = 0;
   if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))
@@ -1470,7 +1471,8 @@ GPTQ_API int gptq_kv_read(gptq_ctx c, const gptq_kv_cache* cache, const int32_t*
   if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
   if (tokens == 0) return GPTQ_OK;
   if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens > INT32_MAX || (tokens + 63) / 64 * cache->heads > (1 << 28))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
   if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
   if (cache->heads == 1) k_head = v_head = 0;
   if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))

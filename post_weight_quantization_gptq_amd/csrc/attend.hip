@@ -61,6 +61,15 @@ __device__ __forceinline__ float sum_groups(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// A load that asks the caches not to keep what is read once (32 contexts of
+// 8192 tokens: 83.4 against 85.7 us; where blocks share the codes it costs: 108
+// rows of 4000 positions 48 against 45 us).
+template <bool ONCE, class V>
+__device__ __forceinline__ V fetch(const V* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(glb(p));
+  return *glb(p);
+}
+
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
@@ -204,6 +213,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   typedef typename T::Chunk Chunk;
   constexpr int CH = T::CH, NI = T::NI, NS = T::NS;
   constexpr int NK = DIM / 32, NO = DIM / 16, NMB = T::NMB;
+  constexpr bool ONCE = NB == 1;  // up to 16 rows: one block, so that the codes are read once
   __shared__ float sm[4][16 * NB], sl[4][16 * NB], scq[16 * NB];
   __shared__ union {
     u32x4 q[NB][NK][64];
@@ -260,12 +270,12 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       const uint8_t* r = kr + 4 * i * T::RB;
 #pragma unroll
       for (int s = 0; s < T::NF; ++s) {
-        const u32x4 u = *glb((const u32x4*)(r + 64 * s + 16 * g));
+        const u32x4 u = fetch<ONCE>((const u32x4*)(r + 64 * s + 16 * g));
 #pragma unroll
         for (int e = 0; e < 4; ++e) t.k[i][4 * s + e] = u[e];
       }
       if constexpr (T::R32) {
-        const u32x2 u = *glb((const u32x2*)(r + 64 * T::NF + 8 * g));
+        const u32x2 u = fetch<ONCE>((const u32x2*)(r + 64 * T::NF + 8 * g));
         t.k[i][4 * T::NF] = u[0];
         t.k[i][4 * T::NF + 1] = u[1];
       }
@@ -286,7 +296,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   auto load_v = [&](T& t, const Place& q) {
     const uint8_t* vr = c.vc + ((((size_t)q.v * c.heads + h) * T::RB + n) << c.pshift) + q.ov;
 #pragma unroll
-    for (int i = 0; i < NMB; ++i) t.v[i] = *glb((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
+    for (int i = 0; i < NMB; ++i) t.v[i] = fetch<ONCE>((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
   };
 
   const bool work = tile < t1;

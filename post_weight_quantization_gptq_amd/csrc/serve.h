@@ -48,6 +48,8 @@ struct KvReadProb {
   void* v;
   const int* slots;
   long long tokens, kt, kh, vt, vh;
+  int wide;    // rows are aligned to eight values
+  int stream;  // stored past the caches
 };
 
 // Attention of seqs x tokens query tokens over the cache.
@@ -74,7 +76,7 @@ hipError_t launch_rope_table(const RopeFreq& f, int length, int half, double mag
 // types: 0 bf16, 1 float32; layout: 0 halves, 1 interleaved
 hipError_t launch_rope(const RopeProb& p, int xtype, int ytype, int layout, hipStream_t st);
 hipError_t launch_kv_write(const KvWriteProb& p, int type, int bits, hipStream_t st);
-hipError_t launch_kv_read(const KvReadProb& p, int type, int bits, hipStream_t st);
+hipError_t launch_kv_read(KvReadProb p, int type, int bits, hipStream_t st);
 void plan_tree_attn(AttnProb& p, int ncu);
 hipError_t launch_attn_join(const AttnProb& p, hipStream_t st);
 hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st);

@@ -3,6 +3,11 @@
 #include "common.h"
 #include "serve.h"
 
+// Outputs from this size on are stored past the caches: they pass through the
+// eight 4 MB L2 before anyone reads them, and would push the inputs out of the
+// caches behind.  134 MB of values read back: 32 us, 71 with ordinary stores.
+#define STREAM_BYTES (32LL << 20)
+
 namespace {
 
 __device__ __forceinline__ float bf_up(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
@@ -31,19 +36,34 @@ __device__ __forceinline__ void load_vals(const float* p, float* o) {
 #pragma unroll
   for (int i = 0; i < N; ++i) o[i] = t.v[i];
 }
-template <int N>
+// STREAM: past the caches (see STREAM_BYTES)
+template <int N, bool STREAM = false, class V>
+__device__ __forceinline__ void store_bits(void* p, const V& t) {
+  typedef uint32_t W __attribute__((ext_vector_type(sizeof(V) >= 16 ? 4 : sizeof(V) >= 8 ? 2 : 1)));
+  if constexpr (STREAM && sizeof(V) % sizeof(W) == 0) {
+    struct Parts {
+      W w[sizeof(V) / sizeof(W)];
+    };
+    const Parts q = __builtin_bit_cast(Parts, t);
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(V) / sizeof(W); ++i) __builtin_nontemporal_store(q.w[i], (W*)p + i);
+  } else {
+    *(V*)p = t;
+  }
+}
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_vals(uint16_t* p, const float* v) {
   Bf<N> t;
 #pragma unroll
   for (int i = 0; i < N; ++i) t.v[i] = bf_down(v[i]);
-  *(Bf<N>*)p = t;
+  store_bits<N, STREAM>(p, t);
 }
-template <int N>
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_vals(float* p, const float* v) {
   Fl<N> t;
 #pragma unroll
   for (int i = 0; i < N; ++i) t.v[i] = v[i];
-  *(Fl<N>*)p = t;
+  store_bits<N, STREAM>(p, t);
 }
 
 }  // namespace
@@ -68,7 +88,7 @@ __global__ __launch_bounds__(256) void k_rope_table(const RopeFreq f, int length
 // (2i, 2i + 1) (interleaved) of the first rot values of every head; the other
 // values are copied.  A thread takes V pairs of one (token, head); a position
 // outside the table gives NaN.
-template <class TX, class TY, int V, bool INTER>
+template <class TX, class TY, int V, bool INTER, bool STREAM>
 __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
   const int half = p.rot / 2;
   const int nrot = half / V, nth = nrot + (p.dim - p.rot) / (2 * V);  // threads of one head
@@ -85,8 +105,8 @@ __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
     const int i = p.rot + (u - nrot) * 2 * V;
     load_vals<V>(x + i, a);
     load_vals<V>(x + i + V, b);
-    store_vals<V>(y + i, a);
-    store_vals<V>(y + i + V, b);
+    store_vals<V, STREAM>(y + i, a);
+    store_vals<V, STREAM>(y + i + V, b);
     return;
   }
   const int i = u * V, pos = p.pos[t];
@@ -120,10 +140,10 @@ __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
       w[2 * j] = r[j];
       w[2 * j + 1] = q[j];
     }
-    store_vals<2 * V>(y + 2 * i, w);
+    store_vals<2 * V, STREAM>(y + 2 * i, w);
   } else {
-    store_vals<V>(y + i, r);
-    store_vals<V>(y + half + i, q);
+    store_vals<V, STREAM>(y + i, r);
+    store_vals<V, STREAM>(y + half + i, q);
   }
 }
 
@@ -163,93 +183,128 @@ __device__ __forceinline__ size_t kv_block(const KvPool& c, int slot, int h) {
   return (size_t)(slot >> c.pshift) * c.heads + h;
 }
 
-// A workgroup takes TW consecutive input tokens of one head.  Sixteen lanes
-// hold a row, four neighbouring values each per 64; K codes go straight to
-// the pool, V codes through LDS, so that the tokens of a dimension, which lie
-// side by side in the pool, leave as 4-byte words where four slots follow
-// each other inside a page.
-template <class T, int BITS, int NCH, int TW>
-__global__ __launch_bounds__(256) void k_kv_write(const KvWriteProb p) {
-  constexpr int PITCH = TW + 4;  // bytes of an LDS row: an odd number of words
-  __shared__ __attribute__((aligned(16))) uint8_t vt[64 * NCH * PITCH];
-  __shared__ int sl[TW];
-  const KvPool& c = p.c;
-  const int tid = threadIdx.x, lane = tid & 15, sub = tid >> 4;
-  const int h = blockIdx.y;
-  const long long t0 = (long long)blockIdx.x * TW;
-  const int nt = (int)min((long long)TW, p.tokens - t0);
-  const int pm = (1 << c.pshift) - 1, D = c.dim;
-  const long long nslot = (long long)c.pages << c.pshift;
-  constexpr float maxq = (float)((1 << BITS) - 1);
-  if (tid < TW) {
-    const int s = tid < nt ? p.slots[t0 + tid] : -1;
-    sl[tid] = s >= 0 && s < nslot ? s : -1;
+// Slots of the TW tokens from t0 on; -1: outside the pool, or no token.
+template <int TW>
+__device__ __forceinline__ void load_slots(const int* slots, long long t0, long long tokens, const KvPool& c, int* sl) {
+  const int i = threadIdx.x;
+  if (i < TW) {
+    const int s = t0 + i < tokens ? slots[t0 + i] : -1;
+    sl[i] = s >= 0 && s < (long long)c.pages << c.pshift ? s : -1;
   }
   __syncthreads();
-  for (int job = sub; job < 2 * TW; job += 16) {
-    const int kv = job >= TW, i = kv ? job - TW : job;
+}
+// Whether four tokens lie side by side in one page.
+__device__ __forceinline__ bool run_of_4(const int* s, int pm) {
+  return s[0] >= 0 && s[1] == s[0] + 1 && s[2] == s[0] + 2 && s[3] == s[0] + 3 && (s[0] & pm) + 3 <= pm;
+}
+// Bytes e of the words w[0..3] become word e (a 4 x 4 transpose).
+__device__ __forceinline__ void transpose4(uint32_t* w) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  w[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  w[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  w[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  w[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// Window of tokens, head and kind (0 keys, 1 values) of a workgroup: all of a
+// window's on one XCD (workgroups go to the eight in turn), one after the other,
+// so that the rows of its heads, which touch, meet in one L2.
+__device__ __forceinline__ long long kv_window(const KvPool& c, int& h, int& kv) {
+  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+  h = i % c.heads;
+  kv = i / c.heads & 1;
+  return (long long)(i / (2 * c.heads)) * 8 + xcd;
+}
+
+// A workgroup takes TW consecutive input tokens of one head, its keys or its
+// values.  G lanes hold a row, eight neighbouring values
+// each.  Key codes go straight to the pool; value codes through LDS, from where
+// blocks of 4 tokens x 4 dimensions are transposed in registers, so that the
+// tokens of a dimension, which lie side by side in the pool, leave as words
+// where four slots follow each other inside a page.
+template <class T, int BITS, int D, int TW>
+__global__ __launch_bounds__(256) void k_kv_write(const KvWriteProb p) {
+  constexpr int G = D <= 64 ? 8 : D <= 128 ? 16 : 32, PITCH = D + 4, RB = D * BITS / 8;
+  __shared__ __attribute__((aligned(16))) uint8_t vt[TW * PITCH];
+  __shared__ int sl[TW];
+  const KvPool& c = p.c;
+  const int tid = threadIdx.x, lane = tid % G;
+  int h, kv;
+  const long long t0 = kv_window(c, h, kv) * TW;
+  if (t0 >= p.tokens) return;
+  const int pm = (1 << c.pshift) - 1;
+  constexpr float maxq = (float)((1 << BITS) - 1);
+  load_slots<TW>(p.slots, t0, p.tokens, c, sl);
+  for (int i = tid / G; i < TW; i += 256 / G) {
     const int slot = sl[i];
     if (slot < 0) continue;
     const T* src = kv ? (const T*)p.v + (t0 + i) * p.vt + h * p.vh : (const T*)p.k + (t0 + i) * p.kt + h * p.kh;
-    float v[NCH][4];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (8 * lane < D) {
+      load_vals<4>(src + 8 * lane, v);
+      load_vals<4>(src + 8 * lane + 4, v + 4);
+    }
     float mn = 0.f, mx = 0.f;
     int bad = 0;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int d = 64 * j + 4 * lane;
-      if (d < D) load_vals<4>(src + d, v[j]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (d >= D) v[j][e] = 0.f;
-        mn = fminf(mn, v[j][e]);
-        mx = fmaxf(mx, v[j][e]);
-        bad |= !(fabsf(v[j][e]) <= 3.402823466e38f);
-      }
+    for (int e = 0; e < 8; ++e) {
+      mn = fminf(mn, v[e]);
+      mx = fmaxf(mx, v[e]);
+      bad |= !(fabsf(v[e]) <= 3.402823466e38f);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
+    for (int o = G / 2; o > 0; o >>= 1) {
       mn = fminf(mn, __shfl_xor(mn, o));
       mx = fmaxf(mx, __shfl_xor(mx, o));
       bad |= __shfl_xor(bad, o);
     }
     const KvGrid g = kv_grid(mn, mx, bad, maxq);
-    const size_t blk = kv_block(c, slot, h);
+    const size_t at = (kv_block(c, slot, h) << c.pshift) + (slot & pm);
     if (lane == 0) {
-      (kv ? c.vs : c.ks)[(blk << c.pshift) + (slot & pm)] = g.s;
-      (kv ? c.vz : c.kz)[(blk << c.pshift) + (slot & pm)] = (uint8_t)g.z;
+      (kv ? c.vs : c.ks)[at] = g.s;
+      (kv ? c.vz : c.kz)[at] = (uint8_t)g.z;
     }
-    uint8_t* krow = c.kc + ((blk << c.pshift) + (slot & pm)) * c.rb;
+    if (8 * lane >= D) continue;
+    uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int d = 64 * j + 4 * lane;
-      if (d >= D) continue;
-      uint32_t q[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = kv_code(v[j][e], g, maxq);
-      if (kv) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vt[(d + e) * PITCH + i] = (uint8_t)q[e];
-      } else if (BITS == 8) {
-        *(uint32_t*)(krow + d) = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-      } else {
-        *(uint16_t*)(krow + (d >> 1)) = (uint16_t)(q[0] | q[1] << 4 | q[2] << 8 | q[3] << 12);
-      }
+    for (int e = 0; e < 8; ++e) q[e] = kv_code(v[e], g, maxq);
+    const uint32_t lo = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, hi = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
+    if (kv) {
+      *(uint32_t*)(vt + i * PITCH + 8 * lane) = lo;
+      *(uint32_t*)(vt + i * PITCH + 8 * lane + 4) = hi;
+    } else if (BITS == 8) {
+      *(uint64_t*)(c.kc + at * RB + 8 * lane) = (uint64_t)hi << 32 | lo;
+    } else {  // two codes a byte
+      const uint32_t a = (lo | lo >> 4) & 0x00FF00FFu, b = (hi | hi >> 4) & 0x00FF00FFu;
+      *(uint32_t*)(c.kc + at * RB + 4 * lane) = ((a | a >> 8) & 0xFFFFu) | (b | b >> 8) << 16;
     }
   }
+  if (!kv) return;
   __syncthreads();
   constexpr int GW = TW / 4;
-  for (int job = tid; job < c.rb * GW; job += 256) {
-    const int r = job / GW, i = 4 * (job % GW);
-    uint32_t w = *(const uint32_t*)(vt + r * PITCH + i);
-    // (the bytes of skipped tokens hold anything)
-    if (BITS == 4) w = (w & 0x0F0F0F0Fu) | (*(const uint32_t*)(vt + (r + (D >> 1)) * PITCH + i) & 0x0F0F0F0Fu) << 4;
-    const int s0 = sl[i];
-    if (s0 >= 0 && sl[i + 1] == s0 + 1 && sl[i + 2] == s0 + 2 && sl[i + 3] == s0 + 3 && (s0 & pm) + 3 <= pm) {
-      __builtin_memcpy(c.vc + ((kv_block(c, s0, h) * c.rb + r) << c.pshift) + (s0 & pm), &w, 4);
+  for (int job = tid; job < RB / 4 * GW; job += 256) {
+    const int r = 4 * (job / GW), i = 4 * (job % GW);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = *(const uint32_t*)(vt + (i + e) * PITCH + r);
+    if (BITS == 4) {  // the dimensions D/2 on in the high halves (the bytes of skipped tokens hold anything)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] |= (*(const uint32_t*)(vt + (i + e) * PITCH + r + D / 2) & 0x0F0F0F0Fu) << 4;
+    }
+    transpose4(w);
+    if (run_of_4(sl + i, pm)) {
+      uint8_t* dst = c.vc + ((kv_block(c, sl[i], h) * RB + r) << c.pshift) + (sl[i] & pm);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) __builtin_memcpy(dst + ((size_t)e << c.pshift), &w[e], 4);
     } else {
-      for (int e = 0; e < 4; ++e) {
-        const int s = sl[i + e];
-        if (s >= 0) c.vc[((kv_block(c, s, h) * c.rb + r) << c.pshift) + (s & pm)] = (uint8_t)(w >> (8 * e));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = sl[i + j];
+        if (s < 0) continue;
+        uint8_t* dst = c.vc + ((kv_block(c, s, h) * RB + r) << c.pshift) + (s & pm);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(size_t)e << c.pshift] = (uint8_t)(w[e] >> (8 * j));
       }
     }
   }
@@ -258,76 +313,84 @@ __global__ __launch_bounds__(256) void k_kv_write(const KvWriteProb p) {
 // ------------------------------------------------------------ cache read --
 // The inverse, laid out the same: fl32(s (q - z)), rounded once to the output
 // type; a slot outside the pool reads as zeros.
-template <class T, int BITS, int NCH, int TW>
+template <class T, int BITS, int D, int TW>
 __global__ __launch_bounds__(256) void k_kv_read(const KvReadProb p) {
-  constexpr int PITCH = TW + 4;
-  __shared__ __attribute__((aligned(16))) uint8_t vt[64 * NCH * BITS / 8 * PITCH];
+  constexpr int RB = D * BITS / 8, PITCH = RB + 4, L = D / 8;
+  __shared__ __attribute__((aligned(16))) uint8_t vt[TW * PITCH];
   __shared__ int sl[TW];
   const KvPool& c = p.c;
-  const int tid = threadIdx.x, lane = tid & 15, sub = tid >> 4;
-  const int h = blockIdx.y;
-  const long long t0 = (long long)blockIdx.x * TW;
+  const int tid = threadIdx.x;
+  int h, kv;
+  const long long t0 = kv_window(c, h, kv) * TW;
+  if (t0 >= p.tokens) return;
   const int nt = (int)min((long long)TW, p.tokens - t0);
-  const int pm = (1 << c.pshift) - 1, D = c.dim;
-  const long long nslot = (long long)c.pages << c.pshift;
-  if (tid < TW) {
-    const int s = tid < nt ? p.slots[t0 + tid] : -1;
-    sl[tid] = s >= 0 && s < nslot ? s : -1;
-  }
-  __syncthreads();
-  constexpr int GW = TW / 4;
-  for (int job = tid; job < c.rb * GW; job += 256) {
-    const int r = job / GW, i = 4 * (job % GW);
-    uint32_t w = 0;
-    const int s0 = sl[i];
-    if (s0 >= 0 && sl[i + 1] == s0 + 1 && sl[i + 2] == s0 + 2 && sl[i + 3] == s0 + 3 && (s0 & pm) + 3 <= pm) {
-      __builtin_memcpy(&w, c.vc + ((kv_block(c, s0, h) * c.rb + r) << c.pshift) + (s0 & pm), 4);
-    } else {
-      for (int e = 0; e < 4; ++e) {
-        const int s = sl[i + e];
-        if (s >= 0) w |= (uint32_t)c.vc[((kv_block(c, s, h) * c.rb + r) << c.pshift) + (s & pm)] << (8 * e);
-      }
-    }
-    *(uint32_t*)(vt + r * PITCH + i) = w;
-  }
-  __syncthreads();
-  for (int job = sub; job < 2 * TW; job += 16) {
-    const int kv = job >= TW, i = kv ? job - TW : job;
-    if (i >= nt) continue;
-    const int slot = sl[i];
-    T* dst = kv ? (T*)p.v + (t0 + i) * p.vt + h * p.vh : (T*)p.k + (t0 + i) * p.kt + h * p.kh;
-    float s = 0.f, z = 0.f;
-    const size_t at = slot < 0 ? 0 : (kv_block(c, slot, h) << c.pshift) + (slot & pm);
-    if (slot >= 0) {
-      s = (kv ? c.vs : c.ks)[at];
-      z = (float)(kv ? c.vz : c.kz)[at];
-    }
-    const uint8_t* krow = c.kc + at * c.rb;
+  const int pm = (1 << c.pshift) - 1;
+  load_slots<TW>(p.slots, t0, p.tokens, c, sl);
+  if (kv) {
+    constexpr int GW = TW / 4;
+    for (int job = tid; job < RB / 4 * GW; job += 256) {
+      const int r = 4 * (job / GW), i = 4 * (job % GW);
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (run_of_4(sl + i, pm)) {
+        const uint8_t* src = c.vc + ((kv_block(c, sl[i], h) * RB + r) << c.pshift) + (sl[i] & pm);
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int d = 64 * j + 4 * lane;
-      if (d >= D) continue;
-      uint32_t q = 0;
-      if (slot >= 0) {
-        if (kv) {
-          const int rows = BITS == 8 ? D : D >> 1;
-          const int r = d < rows ? d : d - rows, sh = d < rows ? 0 : 4;  // 4 bits: the upper half's nibbles
+        for (int e = 0; e < 4; ++e) __builtin_memcpy(&w[e], src + ((size_t)e << c.pshift), 4);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b = vt[(r + e) * PITCH + i];
-            q |= (BITS == 8 ? b : (b >> sh) & 15u) << (8 * e);
-          }
-        } else if (BITS == 8) {
-          q = *(const uint32_t*)(krow + d);
-        } else {
-          const uint32_t w = *(const uint16_t*)(krow + (d >> 1));
-          q = (w & 15u) | (w & 0xF0u) << 4 | (w & 0xF00u) << 8 | (w & 0xF000u) << 12;
+        for (int j = 0; j < 4; ++j) {
+          const int s = sl[i + j];
+          if (s < 0) continue;
+          const uint8_t* src = c.vc + ((kv_block(c, s, h) * RB + r) << c.pshift) + (s & pm);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] |= (uint32_t)src[(size_t)e << c.pshift] << (8 * j);
         }
       }
-      float v[4];
+      transpose4(w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = slot < 0 ? 0.f : __fmul_rn(s, (float)((q >> (8 * e)) & 255u) - z);
+      for (int e = 0; e < 4; ++e) *(uint32_t*)(vt + (i + e) * PITCH + r) = w[e];
+    }
+    __syncthreads();
+  }
+  for (int job = tid; job < nt * L; job += 256) {
+    const int i = job / L, d = 8 * (job % L), slot = sl[i];
+    T* dst = kv ? (T*)p.v + (t0 + i) * p.vt + h * p.vh : (T*)p.k + (t0 + i) * p.kt + h * p.kh;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0) {
+      const size_t at = (kv_block(c, slot, h) << c.pshift) + (slot & pm);
+      const float s = (kv ? c.vs : c.ks)[at], z = (float)(kv ? c.vz : c.kz)[at];
+      uint32_t lo, hi;
+      if (kv) {
+        const int r = BITS == 8 || d < D / 2 ? d : d - D / 2, sh = BITS == 8 || d < D / 2 ? 0 : 4;
+        lo = *(const uint32_t*)(vt + i * PITCH + r);
+        hi = *(const uint32_t*)(vt + i * PITCH + r + 4);
+        if (BITS == 4) {
+          lo = (lo >> sh) & 0x0F0F0F0Fu;
+          hi = (hi >> sh) & 0x0F0F0F0Fu;
+        }
+      } else if (BITS == 8) {
+        const uint64_t u = *(const uint64_t*)(c.kc + at * RB + d);
+        lo = (uint32_t)u;
+        hi = (uint32_t)(u >> 32);
+      } else {
+        const uint32_t u = *(const uint32_t*)(c.kc + at * RB + d / 2);
+        const uint32_t e = u & 0x0F0F0F0Fu, o = (u >> 4) & 0x0F0F0F0Fu;  // even and odd codes
+        lo = __builtin_amdgcn_perm(o, e, 0x05010400u);
+        hi = __builtin_amdgcn_perm(o, e, 0x07030602u);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __fmul_rn(s, (float)((lo >> (8 * e)) & 255u) - z);
+        v[e + 4] = __fmul_rn(s, (float)((hi >> (8 * e)) & 255u) - z);
+      }
+    }
+    if (p.wide) {
+      if (p.stream)
+        store_vals<8, true>(dst + d, v);
+      else
+        store_vals<8>(dst + d, v);
+    } else {
       store_vals<4>(dst + d, v);
+      store_vals<4>(dst + d + 4, v + 4);
     }
   }
 }
@@ -351,14 +414,22 @@ hipError_t rope_v(const RopeProb& p, hipStream_t st) {
            (uintptr_t)p.x % (e * sizeof(TX)) == 0 && (uintptr_t)p.y % (e * sizeof(TY)) == 0 &&
            (uintptr_t)p.table % (4 * v) == 0;
   };
-  const int v = fits(4) ? 4 : 1;
+  // eight where the result is bf16, so that a store is 16 bytes (a prompt of
+  // 8192 x 40 heads of 128 from float32: 45 us, 53 with four)
+  const int v = sizeof(TY) == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
   const int nth = p.dim / (2 * v);
-  const long long n = p.tokens * p.heads * nth;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (v == 4)
-    hipLaunchKernelGGL((k_rope<TX, TY, 4, INTER>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((k_rope<TX, TY, 1, INTER>), grid, dim3(256), 0, st, p);
+  const dim3 grid((unsigned)((p.tokens * p.heads * nth + 255) / 256));
+  const bool stream = p.tokens * p.heads * p.dim * (long long)sizeof(TY) >= STREAM_BYTES;
+  if (v == 8) {
+    if constexpr (sizeof(TY) == 2)
+      hipLaunchKernelGGL((stream ? k_rope<TX, TY, 8, INTER, true> : k_rope<TX, TY, 8, INTER, false>), grid, dim3(256), 0,
+                         st, p);
+  } else if (v == 4) {
+    hipLaunchKernelGGL((stream ? k_rope<TX, TY, 4, INTER, true> : k_rope<TX, TY, 4, INTER, false>), grid, dim3(256), 0,
+                       st, p);
+  } else {
+    hipLaunchKernelGGL((k_rope<TX, TY, 1, INTER, false>), grid, dim3(256), 0, st, p);
+  }
   return hipGetLastError();
 }
 template <class TX, class TY>
@@ -366,35 +437,36 @@ hipError_t rope_l(const RopeProb& p, int layout, hipStream_t st) {
   return layout ? rope_v<TX, TY, true>(p, st) : rope_v<TX, TY, false>(p, st);
 }
 
-template <class T, int BITS, int NCH>
-void kv_write_n(const KvWriteProb& p, hipStream_t st) {
-  const dim3 grid((unsigned)((p.tokens + 63) / 64), p.c.heads);
-  hipLaunchKernelGGL((k_kv_write<T, BITS, NCH, 64>), grid, dim3(256), 0, st, p);
+// 64 tokens a workgroup where that makes 512 of them, else 16
+template <class T, int BITS, int D, class P>
+void kv_launch(const P& p, hipStream_t st, void (*wide)(P), void (*narrow)(P)) {
+  const bool w = (p.tokens + 63) / 64 * p.c.heads >= 256;
+  const dim3 grid((unsigned)(((p.tokens + (w ? 63 : 15)) / (w ? 64 : 16) + 7) / 8 * 8 * p.c.heads * 2));
+  hipLaunchKernelGGL(w ? wide : narrow, grid, dim3(256), 0, st, p);
 }
-template <class T, int BITS>
-hipError_t kv_write_b(const KvWriteProb& p, hipStream_t st) {
-  switch ((p.c.dim + 63) / 64) {
-    case 1: kv_write_n<T, BITS, 1>(p, st); break;
-    case 2: kv_write_n<T, BITS, 2>(p, st); break;
-    case 3: kv_write_n<T, BITS, 3>(p, st); break;
-    default: kv_write_n<T, BITS, 4>(p, st); break;
+template <class T, int BITS, int D>
+void kv_one(const KvWriteProb& p, hipStream_t st) {
+  kv_launch<T, BITS, D>(p, st, k_kv_write<T, BITS, D, 64>, k_kv_write<T, BITS, D, 16>);
+}
+template <class T, int BITS, int D>
+void kv_one(const KvReadProb& p, hipStream_t st) {
+  kv_launch<T, BITS, D>(p, st, k_kv_read<T, BITS, D, 64>, k_kv_read<T, BITS, D, 16>);
+}
+template <class T, int BITS, class P>
+hipError_t kv_dim(const P& p, hipStream_t st) {
+  switch (p.c.dim) {
+    case 64: kv_one<T, BITS, 64>(p, st); break;
+    case 96: kv_one<T, BITS, 96>(p, st); break;
+    case 128: kv_one<T, BITS, 128>(p, st); break;
+    case 192: kv_one<T, BITS, 192>(p, st); break;
+    default: kv_one<T, BITS, 256>(p, st); break;
   }
   return hipGetLastError();
 }
-template <class T, int BITS, int NCH>
-void kv_read_n(const KvReadProb& p, hipStream_t st) {
-  const dim3 grid((unsigned)((p.tokens + 63) / 64), p.c.heads);
-  hipLaunchKernelGGL((k_kv_read<T, BITS, NCH, 64>), grid, dim3(256), 0, st, p);
-}
-template <class T, int BITS>
-hipError_t kv_read_b(const KvReadProb& p, hipStream_t st) {
-  switch ((p.c.dim + 63) / 64) {
-    case 1: kv_read_n<T, BITS, 1>(p, st); break;
-    case 2: kv_read_n<T, BITS, 2>(p, st); break;
-    case 3: kv_read_n<T, BITS, 3>(p, st); break;
-    default: kv_read_n<T, BITS, 4>(p, st); break;
-  }
-  return hipGetLastError();
+template <class P>
+hipError_t kv_any(const P& p, int type, int bits, hipStream_t st) {
+  if (type) return bits == 8 ? kv_dim<float, 8>(p, st) : kv_dim<float, 4>(p, st);
+  return bits == 8 ? kv_dim<uint16_t, 8>(p, st) : kv_dim<uint16_t, 4>(p, st);
 }
 
 }  // namespace
@@ -406,11 +478,11 @@ hipError_t launch_rope(const RopeProb& p, int xtype, int ytype, int layout, hipS
 }
 
 hipError_t launch_kv_write(const KvWriteProb& p, int type, int bits, hipStream_t st) {
-  if (type) return bits == 8 ? kv_write_b<float, 8>(p, st) : kv_write_b<float, 4>(p, st);
-  return bits == 8 ? kv_write_b<uint16_t, 8>(p, st) : kv_write_b<uint16_t, 4>(p, st);
+  return kv_any(p, type, bits, st);
 }
 
-hipError_t launch_kv_read(const KvReadProb& p, int type, int bits, hipStream_t st) {
-  if (type) return bits == 8 ? kv_read_b<float, 8>(p, st) : kv_read_b<float, 4>(p, st);
-  return bits == 8 ? kv_read_b<uint16_t, 8>(p, st) : kv_read_b<uint16_t, 4>(p, st);
+hipError_t launch_kv_read(KvReadProb p, int type, int bits, hipStream_t st) {
+  p.wide = (p.kt | p.kh | p.vt | p.vh) % 8 == 0 && ((uintptr_t)p.k | (uintptr_t)p.v) % (type ? 32 : 16) == 0;
+  p.stream = p.tokens * p.c.heads * p.c.dim * (type ? 8LL : 4LL) >= STREAM_BYTES;
+  return kv_any(p, type, bits, st);
 }
