@@ -1510,8 +1510,8 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   if (seqs == 0 || tokens == 0 || heads == 0) return GPTQ_OK;
   if (mask && (int64_t)words * 32 < tokens) return set_err(c, GPTQ_ERR_INVALID_ARG, "a mask row has too few words");
   if (!Q || !O || !lengths || (width > 0 && !tables)) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if ((int64_t)width * cache->page > INT32_MAX || (int64_t)tokens * heads > ((int64_t)1 << 26) ||
-      (int64_t)seqs * tokens * heads > INT32_MAX)
+  if ((int64_t)width * cache->page > (1 << 29) || (int64_t)tokens * heads > ((int64_t)1 << 26) ||
+      (int64_t)seqs * tokens * heads > (1 << 30))
     return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many rows or positions for one launch");
   if (seqs == 1) q_seq = o_seq = 0;  // the stride of a dimension of one is never used
   if (tokens == 1) q_token = o_token = 0;
@@ -1543,12 +1543,13 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   // saves the second launch (1000 positions, 8 heads of 4 rows: 14.3 against
   // 17.3 us a call).  Where that workgroup would join many rows alone, a launch
   // that fills the chip is faster (108 rows of 4000 positions: 45 against 54 us).
-  const bool fuse = p.nsplit > 1 && p.nsplit <= 8 && p.nb == 1 && p.nrb == 1;
-  if (p.nsplit > 1) {
-    const size_t rows = (size_t)seqs * tokens * heads * p.nsplit;
-    if ((rc = ensure(c, c->attn, rows * (cache->dim + 2) * sizeof(float)))) return rc;
+  const bool split = p.most > 1, fuse = split && p.shares <= 8 && p.nb == 1 && !p.wide;
+  {
+    const size_t rows = split ? (size_t)p.kept * tokens * p.group : 0;
+    if ((rc = ensure(c, c->attn, (rows * (cache->dim + 2) + 2 * (size_t)seqs) * sizeof(float)))) return rc;
     p.part = (float*)c->attn.p;
     p.ml = p.part + rows * cache->dim;
+    p.info = (int*)(p.ml + 2 * rows);
   }
   if (fuse) {
     const size_t had = c->counts.cap;
@@ -1557,7 +1558,7 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
       HIPCHK(c, launch_zero_f32((float*)c->counts.p, (long long)(c->counts.cap / sizeof(float)), c->stream));
     p.count = (int*)c->counts.p;
   }
-  LAUNCH(c, "k_tree_attn", launch_tree_attn(p, cache->bits, c->stream));
-  if (p.nsplit > 1 && !fuse) LAUNCH(c, "k_attn_join", launch_attn_join(p, c->stream));
+  LAUNCH(c, p.wide ? "k_tree_attn_wide" : "k_tree_attn", launch_tree_attn(p, cache->bits, c->stream));
+  if (split && !fuse) LAUNCH(c, "k_attn_join", launch_attn_join(p, c->stream));
   return GPTQ_OK;
 }

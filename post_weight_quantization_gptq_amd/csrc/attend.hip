@@ -108,6 +108,283 @@ struct Tile {
   }
 };
 
+// Positions of a call's sequence b: `len` before the drafted tokens, npos in all.
+struct Span {
+  int b, len, npos;
+};
+__device__ __forceinline__ Span span_of(const AttnProb& p, int b) {
+  const int len = p.lengths[b], cap = p.width << p.c.pshift;
+  return Span{b, len, len < 0 ? 0 : (int)min((long long)len + p.tokens, (long long)cap)};
+}
+// A workgroup's share of the work: the positions of sequence b, key head h, are
+// cut into `shares` runs of tiles of nearly the same number, this is run
+// `split`.  first: number of the sequence's first share of head 0 in the
+// workspace, which holds those of sequences with more than one.
+struct Share {
+  int b, h, split, shares, first;
+  // of its row rr, of R: the shares of a row lie side by side
+  __device__ __forceinline__ long long place(int rr, int R) const {
+    return ((long long)first + (long long)h * shares) * R + (long long)rr * shares + split;
+  }
+};
+// Sums over the lanes up to each one; the last lane's.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // from one lane below, in rows of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // two
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // four
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // eight
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // the last lane of the row below
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // the last lane of the lower half
+  return v;
+}
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
+// Quotient rounded up, of numbers under 2^24.
+__device__ __forceinline__ int ceil_div(int a, int b) {
+  int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b));
+  q -= q * b >= a ? 1 : 0;  // the product may be off by one either way
+  q += q * b < a ? 1 : 0;
+  q += q * b < a ? 1 : 0;
+  return q;
+}
+// Workgroups go to sequences by their lengths, which only the device knows:
+// the fewest tiles for each, at least 256 positions, such that no more of them
+// (p.fit for a key head and row block) are made than run at once.  The longest
+// share is what a call takes: eight trees over 0 to 4093 positions 43 us, 47
+// with equally many shares for each sequence.  The whole wave takes part.
+template <int TP>
+__device__ __forceinline__ bool find_share(const AttnProb& p, int unit, Share& o) {
+  const int lane = threadIdx.x & 63, H = p.c.heads, fit = p.fit;
+  constexpr int LEAST = 256 / TP;
+  auto tiles = [&](int b) { return b < p.seqs ? (span_of(p, b).npos + TP - 1) / TP : 0; };
+  if (p.seqs == 1) {
+    const int t = tiles(0);
+    o.b = o.first = 0;
+    o.shares = max(ceil_div(t, max(LEAST, ceil_div(t, fit))), 1);
+    o.h = unit / o.shares;
+    o.split = unit % o.shares;
+    return o.h < H;
+  }
+  const int mine = tiles(lane);
+  auto tiles_at = [&](int b) { return b == 0 ? mine : tiles(b + lane); };
+  float total = 0.f;
+  for (int b = 0; b < p.seqs; b += 64) total += (float)wave_sum(tiles_at(b));
+  // (a sequence rounds its shares up, so that some more than total / fit are needed)
+  int lo = max(LEAST, (int)min(total * __builtin_amdgcn_rcpf((float)fit), 16777215.f) + 1), hi = 2 * lo;
+  for (int k = 0; k < 6 && lo < hi; ++k) {
+    const int mid = (lo + hi) >> 1;
+    int n = 0;
+    for (int b = 0; b < p.seqs; b += 64)
+      n += wave_sum(b + lane < p.seqs ? max(ceil_div(tiles_at(b), mid), 1) : 0);
+    if (n <= fit)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  const int per = hi;
+  int run = 0, kept = 0;  // shares before; of those, in the workspace
+  for (int b = 0; b < p.seqs; b += 64) {
+    const int sh = b + lane < p.seqs ? max(ceil_div(tiles_at(b), per), 1) : 0;
+    const int in = wave_scan(sh), in2 = wave_scan(sh > 1 ? sh : 0);
+    const long long first = (long long)H * (run + in - sh), last = (long long)H * (run + in);
+    const uint64_t hit = __ballot(unit >= first && unit < last);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      o.b = b + at;
+      o.shares = __builtin_amdgcn_readlane(sh, at);
+      const int local = unit - H * (run + __builtin_amdgcn_readlane(in, at) - o.shares);
+      o.h = local / o.shares;
+      o.split = local % o.shares;
+      o.first = H * (kept + __builtin_amdgcn_readlane(in2, at) - (o.shares > 1 ? o.shares : 0));
+      return true;
+    }
+    run += __builtin_amdgcn_readlane(in, 63);
+    kept += __builtin_amdgcn_readlane(in2, 63);
+  }
+  return false;
+}
+
+// Which of the positions j0 .. j0 + CH - 1 drafted token t sees.
+template <int CH>
+__device__ __forceinline__ uint32_t seen(const AttnProb& p, const Span& a, int j0, int t) {
+  const int below = min(max(a.len - j0, 0), CH);
+  uint32_t bits;
+  if (p.mask) {
+    bits = 0;
+    const int i0 = max(j0 - a.len, 0), wd = i0 >> 5;
+    const uint32_t* m = p.mask + ((size_t)a.b * p.tokens + t) * p.words;
+    if (below < CH) {
+      const uint64_t lo = wd < p.words ? m[wd] : 0u, hi = wd + 1 < p.words ? m[wd + 1] : 0u;
+      bits = (uint32_t)((hi << 32 | lo) >> (i0 & 31));
+    }
+    bits = bits << below | ((1u << below) - 1u);
+  } else {
+    bits = (1u << min(max(a.len + t + 1 - j0, 0), CH)) - 1u;
+  }
+  return bits & ((1u << min(max(a.npos - j0, 0), CH)) - 1u);
+}
+
+// Query row rr of (sequence b, key head h) as operands for NK steps of 32
+// dimensions, and the factor that turns its scores, times their positions'
+// scales, into powers of two.  off(ks, j): dimension of the j-th four values of
+// step ks (8 bits), off(ks, 0) of its eight (4 bits).
+template <int NK, int BITS, class Off>
+__device__ __forceinline__ float query_row(const AttnProb& p, int b, int h, int rr, Off off, u32x4* out) {
+  const int R = p.tokens * p.group, rc = min(rr, R - 1);
+  const uint16_t* q = p.q + b * p.qb + (rc / p.group) * p.qt + (h * p.group + rc % p.group) * p.qh;
+  float v[NK][8];
+  float mx = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks) {
+    uint32_t u[4];
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x2 a = *glb((const u32x2*)(q + off(ks, j)));
+        u[2 * j] = a[0];
+        u[2 * j + 1] = a[1];
+      }
+    } else {
+      const u32x4 a = *glb((const u32x4*)(q + off(ks, 0)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = a[j];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // 4 bits: elements 0, 4, 1, 5, 2, 6, 3, 7 of the eight
+      const int i = BITS == 8 ? e : (e >> 1) + 4 * (e & 1);
+      const float f = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+      v[ks][e] = rr < R ? f : 0.f;
+      mx = fmaxf(mx, fabsf(v[ks][e]));
+    }
+  }
+  mx = max_groups(mx);
+  const int ex = (int)(__float_as_uint(mx) >> 23);
+  const int up = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^up mx in [2^14, 2^15)
+  float f = __uint_as_float((uint32_t)(127 + up) << 23);
+  if (p.scale < 0.f) f = -f;
+  if (p.scale == 0.f) f = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < NK; ++ks) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // 4 bits: the odd codes of a word arrive times 16
+      const float fj = BITS == 4 && (j & 1) ? f * 0.0625f : f;
+      out[ks][j] = pack16(v[ks][2 * j] * fj, v[ks][2 * j + 1] * fj);
+    }
+  }
+  // (a factor under 2^-100 leaves every weight at 1, as 2^-100 does)
+  return fmaxf(fabsf(p.scale) * __uint_as_float((uint32_t)(127 - up) << 23), 0x1p-100f);
+}
+
+// Eight key codes as an operand, less their zero point: zl = 1024 + z twice, zh
+// = 1024 + 16 z twice.
+template <int BITS>
+__device__ __forceinline__ u32x4 key_operand(uint32_t w0, uint32_t w1, uint32_t zl, uint32_t zh) {
+  if constexpr (BITS == 8)
+    return u32x4{sub16(bytes2(w0, 0), zl), sub16(bytes2(w0, 1), zl), sub16(bytes2(w1, 0), zl), sub16(bytes2(w1, 1), zl)};
+  const uint32_t w8 = w0 >> 8;
+  return u32x4{sub16(nib_lo(w0), zl), sub16(nib_hi(w0), zh), sub16(nib_lo(w8), zl), sub16(nib_hi(w8), zh)};
+}
+// The value codes of eight positions (two words) as operands, less their zero
+// points z0, z1: at 8 bits lo, at 4 bits lo and (times 16) hi.
+template <int BITS>
+__device__ __forceinline__ void value_operand(const uint32_t* w, const uint32_t* z, u32x4& lo, u32x4& hi) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (BITS == 8) {
+      lo[2 * j] = diff_bf16(bytes2(w[j], 0), bytes2(z[j], 0));
+      lo[2 * j + 1] = diff_bf16(bytes2(w[j], 1), bytes2(z[j], 1));
+    } else {
+      lo[2 * j] = diff_bf16(nib_lo(w[j]), nib_lo(z[j]));
+      lo[2 * j + 1] = diff_bf16(nib_lo(w[j] >> 8), nib_lo(z[j] >> 8));
+      hi[2 * j] = diff_bf16(nib_hi(w[j]), nib_hi(z[j] << 4));
+      hi[2 * j + 1] = diff_bf16(nib_hi(w[j] >> 8), nib_hi(z[j] >> 4));
+    }
+  }
+}
+
+// The rows of a wave: running reference M (NONE: nothing seen), sum l, factor
+// cq, and the unnormalised result.
+template <int NB, int NO>
+struct Rows {
+  f32x4 acc[NB][NO];
+  float M[NB], l[NB], cq[NB];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      M[nb] = NONE;
+      l[nb] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) acc[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+};
+
+// Scores S of a lane's CH positions (before their scales ks) to weights P times
+// the scales vs, for row block nb: [leading, next][step].
+template <int BITS, int CH, int NB, int NO>
+__device__ __forceinline__ void weigh(Rows<NB, NO>& r, int nb, const f32x4* S, const f32x4* ks, const f32x4* vs,
+                                      bool masked, uint32_t see, u32x4 (*P)[CH / 8]) {
+  float xs[CH], mx = NONE;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) xs[i] = S[i >> 2][i & 3] * ks[i >> 2][i & 3];
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : NONE;
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) mx = fmaxf(mx, xs[i]);
+  // M moves only when a score passes it by 2^8 (its weight): most tiles then
+  // need neither the maximum over the lanes nor a pass over the sums.
+  if (__any((mx - r.M[nb]) * r.cq[nb] > 8.f)) {
+    const float Mn = fmaxf(r.M[nb], max_groups(mx));
+    const float al = Mn > r.M[nb] ? __builtin_amdgcn_exp2f((r.M[nb] - Mn) * r.cq[nb]) : 1.f;
+    r.l[nb] *= al;
+#pragma unroll
+    for (int i = 0; i < NO; ++i) r.acc[nb][i] *= al;
+    r.M[nb] = Mn;
+  }
+  // (nothing seen yet: NONE cq is far below every score's product with cq, and its weights are 0)
+  const float ref = r.M[nb] == NONE ? 0.f : r.M[nb] * r.cq[nb];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], r.cq[nb], -ref));
+    r.l[nb] += e;
+    xs[i] = e * vs[i >> 2][i & 3];
+  }
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < CH / 8; ++s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
+      const float a = xs[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
+      const float b = xs[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
+      P[0][s][j] = lead16(a, b);
+      P[1][s][j] = lead16(rest16(a), rest16(b));
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// End of a wave's positions: sums over the four lanes of a row, M in powers of
+// two (-INFINITY: nothing seen), 4 bits: the upper half's codes came times 16.
+template <int BITS, int NB, int NO>
+__device__ __forceinline__ void settle(Rows<NB, NO>& r) {
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    r.l[nb] = sum_groups(r.l[nb]);
+    r.M[nb] = r.M[nb] == NONE ? -INFINITY : r.M[nb] * r.cq[nb];
+    if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = NO / 2; i < NO; ++i) r.acc[nb][i] *= 0.0625f;
+    }
+  }
+}
+
 // Rows that another workgroup of the same launch reads, perhaps on another
 // XCD: stored through and loaded past the L2 (agent-scope accesses), so that no
 // cache has to be written back or emptied for them.  (A fence pair, which does
@@ -123,28 +400,30 @@ __device__ __forceinline__ f32x2 get2(const float* p) {
   return f32x2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
 }
 
-// Joins the shares of row `row` of (sequence, key head, row), dimensions d .. d
+// Joins the shares of row rr of sequence me.b, key head me.h, dimensions d .. d
 // + 3: sum of exp2(M_s - max M) (O_s, l_s).  G threads take every G-th share
-// each (k says which) and are added in order; row < 0: takes part only.
+// each (k says which) and are added in order; !on: takes part only.
 template <int G>
 struct JoinLds {
   f32x4 o[G > 1 ? 256 : 1];
   float l[G > 1 ? 256 : 1];
 };
 template <int G, bool SHARED>
-__device__ __forceinline__ void join_row(const AttnProb& p, long long row, int d, int k, JoinLds<G>* s) {
-  const int dim = p.c.dim, ns = p.nsplit;
+__device__ __forceinline__ void join_row(const AttnProb& p, bool on, Share me, int rr, int d, int k, JoinLds<G>* s) {
+  const int dim = p.c.dim, R = p.tokens * p.group;
   f32x4 a = {0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
-  if (row >= 0) {
-    const float* ml = p.ml + 2 * row * ns;
+  if (on) {
+    me.split = 0;
+    const long long row = me.place(rr, R);
+    const float* ml = p.ml + 2 * row;
     float mx = -INFINITY;
 #pragma unroll 8
-    for (int e = 0; e < ns; ++e) mx = fmaxf(mx, get2<SHARED>(ml + 2 * e)[0]);
+    for (int e = 0; e < me.shares; ++e) mx = fmaxf(mx, get2<SHARED>(ml + 2 * e)[0]);
     const float ref = mx == -INFINITY ? 0.f : mx;
-    const float* part = p.part + row * ns * dim + d;
+    const float* part = p.part + row * dim + d;
 #pragma unroll 4
-    for (int e = k; e < ns; e += G) {
+    for (int e = k; e < me.shares; e += G) {
       const f32x2 o0 = get2<SHARED>(part + (size_t)e * dim), o1 = get2<SHARED>(part + (size_t)e * dim + 2);
       const f32x2 m = get2<SHARED>(ml + 2 * e);
       const float f = __builtin_amdgcn_exp2f(m[0] - ref);
@@ -162,11 +441,42 @@ __device__ __forceinline__ void join_row(const AttnProb& p, long long row, int d
       l += s->l[threadIdx.x + e * (dim >> 2)];
     }
   }
-  if (row < 0) return;
+  if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int R = p.tokens * p.group, bh = (int)(row / R), rr = (int)(row % R), b = bh / p.c.heads, h = bh % p.c.heads;
-  *(bf16x4*)(p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh + d) =
+  *(bf16x4*)(p.o + me.b * p.ob + (rr / p.group) * p.ot + (me.h * p.group + rr % p.group) * p.oh + d) =
       __builtin_convertvector(a * inv, bf16x4);
+}
+
+// The rows of a share from row0 on: the result (one share), or the unnormalised
+// rows to the workspace.
+template <int NB, int NO>
+__device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& r, const Share& me, int row0) {
+  const int b = me.b, h = me.h;
+  const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15, R = p.tokens * p.group;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int rr = row0 + 16 * nb + n;
+    if (rr >= R) continue;
+    if (me.shares == 1) {
+      const float inv = r.l[nb] == 0.f ? 0.f : 1.f / r.l[nb];
+      uint16_t* o = p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) *(bf16x4*)(o + 16 * i + 4 * g) = __builtin_convertvector(r.acc[nb][i] * inv, bf16x4);
+    } else {
+      const size_t row = (size_t)me.place(rr, R);
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        float* o = p.part + row * (16 * NO) + 16 * i + 4 * g;
+        if (p.count) {
+          put_shared(o, r.acc[nb][i][0], r.acc[nb][i][1]);
+          put_shared(o + 2, r.acc[nb][i][2], r.acc[nb][i][3]);
+        } else {
+          *(f32x4*)o = r.acc[nb][i];
+        }
+      }
+      if (g == 0) put_shared(p.ml + 2 * row, r.M[nb], r.l[nb]);
+    }
+  }
 }
 
 }  // namespace
@@ -203,8 +513,8 @@ __device__ __forceinline__ void join_row(const AttnProb& p, long long row, int d
 // whatever their scales hold.
 //
 // The four waves of a workgroup take every fourth tile of its share of the
-// positions and are joined in LDS in a fixed order; with several shares
-// (nsplit) the unnormalised rows go to the workspace.  The shares of a row are
+// positions and are joined in LDS in a fixed order; of several shares
+// the unnormalised rows go to the workspace.  The shares of a row are
 // joined, in their order, by the workgroup that comes last (p.count, which it
 // sets back to 0), or where they are many by k_attn_join.
 template <int DIM, int BITS, int NB, int TP, int OCC>
@@ -226,16 +536,20 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   // whose L2 then holds the share's codes for all of them.
   const int x = blockIdx.x / (8 * p.nrb), rem = blockIdx.x % (8 * p.nrb);
   const int rb = rem >> 3, unit = 8 * x + (rem & 7);
-  if (unit >= p.seqs * c.heads * p.nsplit) return;
-  const int split = unit % p.nsplit, bh = unit / p.nsplit;
-  const int h = bh % c.heads, b = bh / c.heads;
+  Share me;
+  if (!find_share<TP>(p, unit, me)) return;
+  const int b = __builtin_amdgcn_readfirstlane(me.b), h = __builtin_amdgcn_readfirstlane(me.h);
+  const int split = __builtin_amdgcn_readfirstlane(me.split), shares = __builtin_amdgcn_readfirstlane(me.shares);
+  if (h == 0 && split == 0 && rb == 0 && tid == 0) {  // for the join
+    p.info[2 * b] = me.first;
+    p.info[2 * b + 1] = shares;
+  }
   const int R = p.tokens * p.group;
 
-  const int len = p.lengths[b];
-  const int cap = p.width << c.pshift;
-  const int npos = len < 0 ? 0 : (int)min((long long)len + p.tokens, (long long)cap);
+  const Span sp = span_of(p, b);
+  const int npos = sp.npos;
   const int ntile = (npos + TP - 1) / TP;
-  const int per = (ntile + p.nsplit - 1) / p.nsplit;
+  const int per = (ntile + shares - 1) / shares;
   const int t1 = min(ntile, (split + 1) * per);
   int tile = split * per + w;
 
@@ -312,85 +626,20 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   // queries: row n of block nb, in the order of the key codes' words
 #pragma unroll 1
   for (int nb = w; nb < NB; nb += 4) {
-    const int rr = 16 * (NB * rb + nb) + n, rc = min(rr, R - 1);
-    const uint16_t* q = p.q + b * p.qb + (rc / p.group) * p.qt + (h * p.group + rc % p.group) * p.qh;
-    float v[NK][8];
-    float mx = 0.f;
+    u32x4 q[NK];
+    const float f = query_row<NK, BITS>(
+        p, b, h, 16 * (NB * rb + nb) + n,
+        [&](int ks, int j) { return BITS == 8 ? T::off(2 * ks + j, g) : 2 * T::off(ks, g); }, q);
 #pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      uint32_t u[4];
-      if constexpr (BITS == 8) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const u32x2 a = *glb((const u32x2*)(q + T::off(2 * ks + j, g)));
-          u[2 * j] = a[0];
-          u[2 * j + 1] = a[1];
-        }
-      } else {
-        const u32x4 a = *glb((const u32x4*)(q + 2 * T::off(ks, g)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = a[j];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // 4 bits: elements 0, 4, 1, 5, 2, 6, 3, 7 of the eight
-        const int i = BITS == 8 ? e : (e >> 1) + 4 * (e & 1);
-        const float f = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
-        v[ks][e] = rr < R ? f : 0.f;
-        mx = fmaxf(mx, fabsf(v[ks][e]));
-      }
-    }
-    mx = max_groups(mx);
-    const int ex = (int)(__float_as_uint(mx) >> 23);
-    const int up = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^up mx in [2^14, 2^15)
-    float f = __uint_as_float((uint32_t)(127 + up) << 23);
-    if (p.scale < 0.f) f = -f;
-    if (p.scale == 0.f) f = 0.f;
-    // (a factor under 2^-100 leaves every weight at 1, as 2^-100 does)
-    if (g == 0) scq[16 * nb + n] = fmaxf(fabsf(p.scale) * __uint_as_float((uint32_t)(127 - up) << 23), 0x1p-100f);
-#pragma unroll
-    for (int ks = 0; ks < NK; ++ks) {
-      u32x4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // 4 bits: the odd codes of a word arrive times 16
-        const float fj = BITS == 4 && (j & 1) ? f * 0.0625f : f;
-        o[j] = pack16(v[ks][2 * j] * fj, v[ks][2 * j + 1] * fj);
-      }
-      sh.q[nb][ks][lane] = o;
-    }
+    for (int ks = 0; ks < NK; ++ks) sh.q[nb][ks][lane] = q[ks];
+    if (g == 0) scq[16 * nb + n] = f;
   }
   __syncthreads();
 
-  f32x4 acc[NB][NO];
-  float M[NB], l[NB], cq[NB];
+  Rows<NB, NO> r;
+  r.clear();
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    M[nb] = NONE;
-    l[nb] = 0.f;
-    cq[nb] = scq[16 * nb + n];
-#pragma unroll
-    for (int i = 0; i < NO; ++i) acc[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // which of the positions j0 .. j0 + CH - 1 does the drafted token of row rr see
-  auto seen = [&](int j0, int rr) -> uint32_t {
-    const int below = min(max(len - j0, 0), CH), tk = min(rr, R - 1) / p.group;
-    uint32_t bits;
-    if (p.mask) {
-      bits = 0;
-      const int i0 = max(j0 - len, 0), wd = i0 >> 5;
-      const uint32_t* m = p.mask + ((size_t)b * p.tokens + tk) * p.words;
-      if (below < CH) {
-        const uint64_t lo = wd < p.words ? m[wd] : 0u, hi = wd + 1 < p.words ? m[wd + 1] : 0u;
-        bits = (uint32_t)((hi << 32 | lo) >> (i0 & 31));
-      }
-      bits = bits << below | ((1u << below) - 1u);
-    } else {
-      bits = (1u << min(max(len + tk + 1 - j0, 0), CH)) - 1u;
-    }
-    return bits & ((1u << min(max(npos - j0, 0), CH)) - 1u);
-  };
+  for (int nb = 0; nb < NB; ++nb) r.cq[nb] = scq[16 * nb + n];
 
   f32x4 S[NB][NI];
   u32x4 P[NB][2][NS];  // [leading, next][step]
@@ -411,116 +660,39 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       for (int nb = 0; nb < NB; ++nb) q[nb] = sh.q[nb][ks][lane];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        u32x4 a;
-        if constexpr (BITS == 8) {
-          const uint32_t w0 = t.k[i][2 * ks], w1 = t.k[i][2 * ks + 1];
-          a = u32x4{sub16(bytes2(w0, 0), zl[i]), sub16(bytes2(w0, 1), zl[i]), sub16(bytes2(w1, 0), zl[i]),
-                    sub16(bytes2(w1, 1), zl[i])};
-        } else {
-          const uint32_t w0 = t.k[i][ks], w8 = w0 >> 8;
-          a = u32x4{sub16(nib_lo(w0), zl[i]), sub16(nib_hi(w0), zh[i]), sub16(nib_lo(w8), zl[i]),
-                    sub16(nib_hi(w8), zh[i])};
-        }
+        const u32x4 a = BITS == 8 ? key_operand<BITS>(t.k[i][2 * ks % T::NW], t.k[i][(2 * ks + 1) % T::NW], zl[i], zh[i])
+                                  : key_operand<BITS>(t.k[i][ks], 0, zl[i], zh[i]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, q[nb], S[nb][i]);
       }
     }
   };
   auto weights = [&](const T& t, int tl) {
-    const bool masked = TP * (tl + 1) > min(len, npos) || __any(t.bad);
+    const bool masked = TP * (tl + 1) > min(sp.len, npos) || __any(t.bad);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float xs[CH], mx = NONE;
       uint32_t see = 0;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) xs[i] = S[nb][i >> 2][i & 3] * t.ks[i >> 2][i & 3];
-      if (masked) {
-        see = t.bad ? 0u : seen(TP * tl + CH * g, 16 * (NB * rb + nb) + n);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : NONE;
-      }
-#pragma unroll
-      for (int i = 0; i < CH; ++i) mx = fmaxf(mx, xs[i]);
-      // M moves only when a score passes it by 2^8 (its weight): most tiles then
-      // need neither the maximum over the lanes nor a pass over the sums.
-      if (__any((mx - M[nb]) * cq[nb] > 8.f)) {
-        const float Mn = fmaxf(M[nb], max_groups(mx));
-        const float al = Mn > M[nb] ? __builtin_amdgcn_exp2f((M[nb] - Mn) * cq[nb]) : 1.f;
-        l[nb] *= al;
-#pragma unroll
-        for (int i = 0; i < NO; ++i) acc[nb][i] *= al;
-        M[nb] = Mn;
-      }
-      // (nothing seen yet: NONE cq is far below every score's product with cq, and its weights are 0)
-      const float ref = M[nb] == NONE ? 0.f : M[nb] * cq[nb];
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(xs[i], cq[nb], -ref));
-        l[nb] += e;
-        xs[i] = e * t.vs[i >> 2][i & 3];
-      }
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) xs[i] = (see >> i) & 1u ? xs[i] : 0.f;
-      }
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
-          const float a = xs[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
-          const float b = xs[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
-          P[nb][0][s][j] = lead16(a, b);
-          P[nb][1][s][j] = lead16(rest16(a), rest16(b));
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // zero points of the value operand's positions, in the form its codes have
-  uint32_t zl[2 * NI], zh[BITS == 4 ? 2 * NI : 1];
-  auto zeros = [&](const T& t) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      if constexpr (BITS == 8) {
-        zl[2 * j] = bytes2(t.vz[j], 0);
-        zl[2 * j + 1] = bytes2(t.vz[j], 1);
-      } else {
-        zl[2 * j] = nib_lo(t.vz[j]);
-        zl[2 * j + 1] = nib_lo(t.vz[j] >> 8);
-        zh[2 * j] = nib_hi(t.vz[j] << 4);
-        zh[2 * j + 1] = nib_hi(t.vz[j] >> 4);
-      }
+      if (masked && !t.bad)
+        see = seen<CH>(p, sp, TP * tl + CH * g, min(16 * (NB * rb + nb) + n, R - 1) / p.group);
+      weigh<BITS, CH>(r, nb, S[nb], t.ks, t.vs, masked, see, P[nb]);
     }
   };
   // vector instructions a product: what unpacking takes, over the products
   constexpr int VPM = NB == 1 ? 8 : NB == 2 ? 4 : 3;
-  auto values = [&](const T& t) {
+  auto values = [&](const T& t, const uint32_t* vz) {
 #pragma unroll
     for (int i = 0; i < NMB; ++i) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         u32x4 a, e;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t u = t.v[i][2 * s + j];
-          const uint32_t *lo = zl + 4 * s + 2 * j, *hi = zh + (BITS == 4 ? 4 * s + 2 * j : 0);
-          if constexpr (BITS == 8) {
-            a[2 * j] = diff_bf16(bytes2(u, 0), lo[0]);
-            a[2 * j + 1] = diff_bf16(bytes2(u, 1), lo[1]);
-          } else {
-            a[2 * j] = diff_bf16(nib_lo(u), lo[0]);
-            a[2 * j + 1] = diff_bf16(nib_lo(u >> 8), lo[1]);
-            e[2 * j] = diff_bf16(nib_hi(u), hi[0]);
-            e[2 * j + 1] = diff_bf16(nib_hi(u >> 8), hi[1]);
-          }
-        }
+        const uint32_t v[2] = {t.v[i][2 * s], t.v[i][2 * s + 1]};
+        value_operand<BITS>(v, vz + 2 * s, a, e);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            acc[nb][i] = mfma_bf(a, P[nb][k][s], acc[nb][i]);
-            if constexpr (BITS == 4) acc[nb][i + NMB] = mfma_bf(e, P[nb][k][s], acc[nb][i + NMB]);
+            r.acc[nb][i] = mfma_bf(a, P[nb][k][s], r.acc[nb][i]);
+            if constexpr (BITS == 4) r.acc[nb][i + NMB] = mfma_bf(e, P[nb][k][s], r.acc[nb][i + NMB]);
           }
         }
       }
@@ -544,11 +716,13 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       if (more) load_k(t, at);
       __builtin_amdgcn_sched_barrier(0);
       weights(t, tile);
-      zeros(t);
+      uint32_t vz[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) vz[i] = t.vz[i];
       __builtin_amdgcn_sched_barrier(0);
       if (more) load_g(t, at);
       __builtin_amdgcn_sched_barrier(0);
-      values(t);
+      values(t, vz);
       __builtin_amdgcn_sched_barrier(0);
       if (!more) break;
       load_v(t, at);
@@ -557,18 +731,12 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
     }
   }
 
-  // one row's sum from its four lanes
+  settle<BITS>(r);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    l[nb] = sum_groups(l[nb]);
-    M[nb] = M[nb] == NONE ? -INFINITY : M[nb] * cq[nb];
-    if constexpr (BITS == 4) {  // the upper half's codes came times 16
-#pragma unroll
-      for (int i = NMB; i < NO; ++i) acc[nb][i] *= 0.0625f;
-    }
     if (g == 0) {
-      sm[w][16 * nb + n] = M[nb];
-      sl[w][16 * nb + n] = l[nb];
+      sm[w][16 * nb + n] = r.M[nb];
+      sl[w][16 * nb + n] = r.l[nb];
     }
   }
   __syncthreads();
@@ -580,19 +748,19 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
     const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
     for (int k = 0; k < 4; ++k) s += sl[k][16 * nb + n] * __builtin_amdgcn_exp2f(sm[k][16 * nb + n] - ref);
-    const float f = __builtin_amdgcn_exp2f(M[nb] - ref);
+    const float f = __builtin_amdgcn_exp2f(r.M[nb] - ref);
 #pragma unroll
-    for (int i = 0; i < NO; ++i) acc[nb][i] *= f;
-    M[nb] = mx;
-    l[nb] = s;
+    for (int i = 0; i < NO; ++i) r.acc[nb][i] *= f;
+    r.M[nb] = mx;
+    r.l[nb] = s;
   }
   auto put = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < NB * NO; ++i) sh.o[k][i][lane] = acc[i / NO][i % NO];
+    for (int i = 0; i < NB * NO; ++i) sh.o[k][i][lane] = r.acc[i / NO][i % NO];
   };
   auto add = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < NB * NO; ++i) acc[i / NO][i % NO] += sh.o[k][i][lane];
+    for (int i = 0; i < NB * NO; ++i) r.acc[i / NO][i % NO] += sh.o[k][i][lane];
   };
   if (w >= 2) put(w - 2);
   __syncthreads();
@@ -602,36 +770,16 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   __syncthreads();
   if (w == 0) {
     add(0);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int rr = 16 * (NB * rb + nb) + n;
-      if (rr >= R) continue;
-      if (p.nsplit == 1) {
-        const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
-        uint16_t* o = p.o + b * p.ob + (rr / p.group) * p.ot + (h * p.group + rr % p.group) * p.oh;
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-          *(bf16x4*)(o + 16 * i + 4 * g) = __builtin_convertvector(acc[nb][i] * inv, bf16x4);
-      } else {
-        const size_t row = ((size_t)bh * R + rr) * p.nsplit + split;
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          float* o = p.part + row * DIM + 16 * i + 4 * g;
-          put_shared(o, acc[nb][i][0], acc[nb][i][1]);
-          put_shared(o + 2, acc[nb][i][2], acc[nb][i][3]);
-        }
-        if (g == 0) put_shared(p.ml + 2 * row, M[nb], l[nb]);
-      }
-    }
+    put_rows(p, r, me, 16 * NB * rb);
   }
-  if (!p.count) return;
+  if (!p.count || shares == 1) return;
   __shared__ int last;
   if (w == 0) {
     // this wave wrote the rows: they are in memory before the count says so
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if (lane == 0) {
-      int* ct = p.count + (size_t)bh * p.nrb + rb;
-      last = __hip_atomic_fetch_add(ct, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.nsplit - 1;
+      int* ct = p.count + ((size_t)b * c.heads + h) * p.nrb + rb;
+      last = __hip_atomic_fetch_add(ct, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == shares - 1;
       if (last) __hip_atomic_store(ct, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
@@ -639,7 +787,212 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   if (!last) return;
   const int r1 = min(16 * NB, R - 16 * NB * rb);
   for (int i = tid; i < r1 * (DIM / 4); i += 256)
-    join_row<1, true>(p, (long long)bh * R + 16 * NB * rb + i / (DIM / 4), 4 * (i % (DIM / 4)), 0, nullptr);
+    join_row<1, true>(p, true, me, 16 * NB * rb + i / (DIM / 4), 4 * (i % (DIM / 4)), 0, nullptr);
+}
+
+// The same attention for many rows: the four waves of a workgroup take 16 NB
+// rows each and the same positions, so that codes are read and unpacked once
+// for 64 NB rows.  Each wave unpacks its part of the next tile into LDS, as the
+// operands are read (a lane's 16 bytes side by side), while the current one is
+// used from the other half; one barrier a tile.  Nothing has to be joined in
+// the workgroup.  The operand layout is that of k_tree_attn with dimension 32
+// ks + 8 g + e in step ks.
+template <int DIM, int BITS, int NB, int TP>
+__global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
+  typedef Tile<DIM, BITS, TP> T;
+  typedef typename T::Chunk Chunk;
+  constexpr int CH = T::CH, NI = T::NI, NS = T::NS, NMB = T::NMB;
+  constexpr int NK = DIM / 32, NO = DIM / 16;
+  constexpr int KS = NK * NI / 4;          // steps of a key block that a wave unpacks
+  constexpr int VM = (NMB + 3) / 4;        // blocks of value rows that a wave unpacks, at most
+  constexpr int KW = BITS == 8 ? 2 : 1;    // words of a lane per step
+  struct Half {
+    u32x4 k[NI][NK][64];
+    u32x4 v[NO][NS][64];
+    float sc[2][TP];
+    int bad[4];
+  };
+  __shared__ Half lds[2];
+  const KvPool& c = p.c;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int x = blockIdx.x / (8 * p.nrb), rem = blockIdx.x % (8 * p.nrb);
+  const int rb = rem >> 3, unit = 8 * x + (rem & 7);
+  Share me;
+  if (!find_share<TP>(p, unit, me)) return;
+  const int b = __builtin_amdgcn_readfirstlane(me.b), h = __builtin_amdgcn_readfirstlane(me.h);
+  const int split = __builtin_amdgcn_readfirstlane(me.split), shares = __builtin_amdgcn_readfirstlane(me.shares);
+  if (h == 0 && split == 0 && rb == 0 && tid == 0) {  // for the join
+    p.info[2 * b] = me.first;
+    p.info[2 * b + 1] = shares;
+  }
+  const int R = p.tokens * p.group, row0 = 16 * NB * (4 * rb + w);
+
+  const Span sp = span_of(p, b);
+  const int npos = sp.npos;
+  const int ntile = (npos + TP - 1) / TP;
+  const int per = (ntile + shares - 1) / shares;
+  const int t0 = split * per, t1 = min(ntile, t0 + per);
+  const int pm = (1 << c.pshift) - 1, lastchunk = max(npos - 1, 0) / CH;
+  const int* table = p.tables + (size_t)b * p.width;
+
+  // What a wave brings of a tile: its steps of key block ki, its blocks of value
+  // rows, and (waves 0 and 1) the scales of the keys and of the values.
+  const int ki = w % NI, k0 = w / NI * KS;
+  struct Raw {
+    uint32_t k[KS][KW];
+    Chunk v[VM];
+    Chunk vz;
+    uint32_t kz;
+    float sc;
+    bool bad;
+  };
+  struct Pages {
+    int k, v, s;
+  };
+  auto chunk_of = [&](int chunk) { return min(chunk, lastchunk) * CH; };
+  // page numbers are asked for a tile before the codes, ahead of the codes of the tile between
+  auto find = [&](int tl) {
+    Pages q;
+    q.k = glb(table)[chunk_of(4 * tl + (n >> 2)) >> c.pshift];
+    q.v = glb(table)[chunk_of(4 * tl + g) >> c.pshift];
+    q.s = glb(table)[chunk_of(4 * tl + min(lane / CH, 3)) >> c.pshift];
+    return q;
+  };
+  auto inside = [&](int pg) { return (unsigned)pg < (unsigned)c.pages; };
+  auto load = [&](Raw& t, int tl, const Pages& q) {
+    const size_t pk = (size_t)(inside(q.k) ? q.k : 0) * c.heads + h, pv = (size_t)(inside(q.v) ? q.v : 0) * c.heads + h;
+    const size_t ps = (size_t)(inside(q.s) ? q.s : 0) * c.heads + h;
+    const size_t at = (pk << c.pshift) + (chunk_of(4 * tl + (n >> 2)) & pm) + 4 * ki + (n & 3);
+    typedef uint32_t KeyWords __attribute__((ext_vector_type(KW)));
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const KeyWords u = *glb((const KeyWords*)(c.kc + at * T::RB + 4 * KW * (4 * (k0 + ks) + g)));
+#pragma unroll
+      for (int e = 0; e < KW; ++e) t.k[ks][e] = u[e];
+    }
+    t.kz = *glb(c.kz + at);
+    const int ov = chunk_of(4 * tl + g) & pm;
+    const uint8_t* vr = c.vc + ((pv * T::RB + n) << c.pshift) + ov;
+#pragma unroll
+    for (int j = 0; j < VM; ++j)
+      t.v[j] = *glb((const Chunk*)(vr + ((size_t)(16 * min(w + 4 * j, NMB - 1)) << c.pshift)));
+    t.vz = *glb((const Chunk*)(c.vz + (pv << c.pshift) + ov));
+    t.bad = !inside(q.s);
+    if (w < 2)
+      t.sc = *glb((w ? c.vs : c.ks) + (ps << c.pshift) + (chunk_of(4 * tl + min(lane / CH, 3)) & pm) + lane % CH);
+  };
+  auto unpack = [&](const Raw& t, Half& o) {
+    const uint32_t zl = t.kz * 0x00010001u + 0x64006400u, zh = t.kz * 0x00100010u + 0x64006400u;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) o.k[ki][k0 + ks][lane] = key_operand<BITS>(t.k[ks][0], t.k[ks][KW - 1], zl, zh);
+#pragma unroll
+    for (int j = 0; j < VM; ++j) {
+      const int mb = w + 4 * j;
+      if (NMB % 4 != 0 && mb >= NMB) break;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const uint32_t v[2] = {t.v[j][2 * s], t.v[j][2 * s + 1]}, z[2] = {t.vz[2 * s], t.vz[2 * s + 1]};
+        u32x4 lo, hi;
+        value_operand<BITS>(v, z, lo, hi);
+        o.v[mb][s][lane] = lo;
+        if constexpr (BITS == 4) o.v[mb + NMB][s][lane] = hi;
+      }
+    }
+    if (w < 2 && lane < TP) {
+      o.sc[w][lane] = t.sc;
+      if (w == 1 && lane % CH == 0) o.bad[lane / CH] = t.bad;
+    }
+  };
+  // LDS written by the others can be read after it; loads in flight stay there
+  auto meet = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+
+  u32x4 qf[NB][NK];
+  Rows<NB, NO> r;
+  r.clear();
+  const bool rows = row0 < R;  // (a wave without rows still brings its part)
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    r.cq[nb] = query_row<NK, BITS>(
+        p, b, h, row0 + 16 * nb + n, [&](int ks, int j) { return 32 * ks + 8 * g + 4 * j; }, qf[nb]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  auto use = [&](const Half& t, int tl) {
+    f32x4 S[NB][NI], kv[2][NI];
+    u32x4 P[NB][2][NS];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const u32x4 a = t.k[i][ks][lane];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) S[nb][i] = mfma(a, qf[nb][ks], S[nb][i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      kv[0][i] = *(const f32x4*)&t.sc[0][CH * g + 4 * i];
+      kv[1][i] = *(const f32x4*)&t.sc[1][CH * g + 4 * i];
+    }
+    const bool bad = t.bad[g], masked = TP * (tl + 1) > min(sp.len, npos) || __any(bad);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t see = 0;
+      if (masked && !bad) see = seen<CH>(p, sp, TP * tl + CH * g, min(row0 + 16 * nb + n, R - 1) / p.group);
+      weigh<BITS, CH>(r, nb, S[nb], kv[0], kv[1], masked, see, P[nb]);
+    }
+#pragma unroll
+    for (int i = 0; i < NO; ++i) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const u32x4 a = t.v[i][s][lane];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) r.acc[nb][i] = mfma_bf(a, P[nb][k][s], r.acc[nb][i]);
+        }
+      }
+    }
+  };
+
+  if (t0 < t1) {
+    Raw t;
+    Pages q = find(t0), q1 = find(t0 + 1);
+    load(t, t0, q);
+    unpack(t, lds[0]);
+    if (t0 + 1 < t1) {
+      q = find(t0 + 2);
+      load(t, t0 + 1, q1);
+    }
+    meet();
+    for (int tl = t0; tl < t1; ++tl) {
+      const int half = (tl - t0) & 1;
+      if (tl + 1 < t1) {
+        unpack(t, lds[half ^ 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (tl + 2 < t1) {
+          q1 = find(tl + 3);
+          load(t, tl + 2, q);
+          q = q1;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (rows) use(lds[half], tl);
+      meet();
+    }
+  }
+  settle<BITS>(r);
+  put_rows(p, r, me, row0);
 }
 
 template <int G>
@@ -647,29 +1000,59 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
   __shared__ JoinLds<G> s;
   const int q4 = p.c.dim >> 2, rows = max(256 / (q4 * G), 1);
   const int i = threadIdx.x / (q4 * G), k = threadIdx.x / q4 % G, d = 4 * (threadIdx.x % q4);
+  const int R = p.tokens * p.group;
   const long long row = (long long)blockIdx.x * rows + i;
-  join_row<G, false>(p, i < rows && row < (long long)p.seqs * p.c.heads * p.tokens * p.group ? row : -1, d, k, &s);
+  bool on = i < rows && row < (long long)p.seqs * p.c.heads * R;
+  Share me{};
+  if (on) {
+    const int bh = (int)(row / R);
+    me = Share{bh / p.c.heads, bh % p.c.heads, 0, p.info[2 * (bh / p.c.heads) + 1], p.info[2 * (bh / p.c.heads)]};
+    on = me.shares > 1;  // a single share has written its result
+  }
+  join_row<G, false>(p, on, me, (int)(row % R), d, k, &s);
 }
 
-// Shares and row blocks of a call: as few blocks as blocks of up to 48 rows
-// (32 for head sizes above 128, whose sums need the registers) allow, of equal size.
+// Rows of a call, and shares of its positions.  k_tree_attn takes as few blocks
+// of up to 48 rows (32 for head sizes above 128, whose sums need the registers)
+// as hold the rows of a (sequence, key head), of equal size; where that is more
+// than one, k_tree_attn_wide takes 64 or 128 rows a block if it pads them to no
+// more.  24 sequences of 8 heads, 2048 to 4096 positions of 128, 8 bits, narrow
+// and wide: 64 rows 84.0 and 76.5 us, 96 rows 101.5 and 105.1, 128 rows 136.4
+// and 115.2, 192 rows 181.4 and 207.6, 256 rows 229.9 and 218.3.
 void plan_tree_attn(AttnProb& p, int ncu) {
-  const long long R = (long long)p.tokens * p.group;
-  const long long r16 = (R + 15) / 16, most = p.c.dim <= 128 ? 3 : 2;
+  const long long R = (long long)p.tokens * p.group, r16 = (R + 15) / 16, most = p.c.dim <= 128 ? 3 : 2;
   p.nrb = (int)((r16 + most - 1) / most);
   p.nb = (int)((r16 + p.nrb - 1) / p.nrb);
-  const long long items = (long long)p.seqs * p.c.heads * p.nrb;
-  const long long tiles = (((long long)p.width << p.c.pshift) + 63) / 64;
-  long long s = (2LL * ncu + items - 1) / items;
-  s = s < (tiles + 3) / 4 ? s : (tiles + 3) / 4;
-  p.nsplit = (int)(s < 1 ? 1 : s > 128 ? 128 : s);
+  const long long wide = R > 64 && p.c.dim <= 128 ? 8 : 4, wrb = (r16 + wide - 1) / wide;
+  p.wide = p.nrb > 1 && wrb * wide <= (long long)p.nrb * p.nb;
+  if (p.wide) {
+    p.nrb = (int)wrb;
+    p.nb = (int)wide / 4;
+  }
+  // shares of one head and row block: what runs at once, and one more for each
+  // sequence by rounding up; those of sequences with more than one are at most
+  // twice what runs at once, or, at 256 positions each, what the tables hold
+  const long long slots = (p.c.dim > 128 && !p.wide && p.nb == 2 ? 1 : 2) * ncu;
+  const long long fit = std::max(slots / ((long long)p.c.heads * p.nrb), 1LL);
+  p.fit = (int)fit;
+  const long long hold = (((long long)p.width << p.c.pshift) + 255) / 256;
+  p.units = (int)((std::min(fit, hold * p.seqs) + p.seqs) * p.c.heads);
+  p.kept = (int)(std::min(2 * fit, hold * p.seqs) * p.c.heads);
+  p.most = (int)std::min(fit, hold);
+  p.shares = (int)std::min(hold, std::max(fit / p.seqs, 1LL));
 }
 
 namespace {
 template <int DIM, int BITS>
 void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
-  if (p.nb == 1)
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, DIM <= 128 ? 64 : 32, 2>), grid, dim3(256), 0, st, p);
+  constexpr int TP = DIM <= 128 ? 64 : 32;
+  if (p.wide) {
+    if (p.nb == 1)
+      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 1, TP>), grid, dim3(256), 0, st, p);
+    else if constexpr (DIM <= 128)
+      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 2, TP>), grid, dim3(256), 0, st, p);
+  } else if (p.nb == 1)
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, TP, 2>), grid, dim3(256), 0, st, p);
   else if (p.nb == 2)
     hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, DIM <= 128 ? 2 : 1>), grid, dim3(256), 0, st, p);
   else if constexpr (DIM <= 128)
@@ -677,8 +1060,7 @@ void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
 }
 template <int BITS>
 hipError_t attn_dim(const AttnProb& p, hipStream_t st) {
-  const long long units = (long long)p.seqs * p.c.heads * p.nsplit;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.nrb));
+  const dim3 grid((unsigned)((p.units + 7) / 8 * 8 * p.nrb));
   switch (p.c.dim) {
     case 64: attn_nb<64, BITS>(p, grid, st); break;
     case 96: attn_nb<96, BITS>(p, grid, st); break;
@@ -697,7 +1079,7 @@ hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st) {
 hipError_t launch_attn_join(const AttnProb& p, hipStream_t st) {
   // eight threads for a value where there are many shares: 160 rows of 128
   // shares 8 us, 15 with one; 13824 rows of three shares 5 us, 11 with eight
-  const int G = p.nsplit >= 16 && p.c.dim <= 128 ? 8 : p.nsplit >= 16 ? 4 : 1;
+  const int G = p.shares >= 16 ? (p.c.dim <= 128 ? 8 : 4) : 1;
   const int rows = std::max(256 / (p.c.dim / 4 * G), 1);
   const long long n = (long long)p.seqs * p.c.heads * p.tokens * p.group;
   const dim3 grid((unsigned)((n + rows - 1) / rows));

@@ -64,11 +64,16 @@ struct AttnProb {
   int seqs, tokens, heads, group;  // group = heads / c.heads
   int width, words;
   float scale;  // of the scores, times log2(e)
-  // plan: row blocks of 16 nb rows, shares of the positions, and the shares'
-  // unnormalised rows [sequence][key head][row][share][dim] with their {M, l}
-  int nb, nrb, nsplit;
+  // Plan: row blocks of 16 nb rows (64 nb in the kernel for many rows), shares
+  // of a key head and row block that run at once, the most units (shares of a key
+  // head) there can be, the most of them in the workspace, and the most shares
+  // and the expected number of a sequence.
+  int nb, nrb, wide, fit, units, kept, most, shares;
+  // workspace: unnormalised rows [unit][row][dim] with their {M, l}, and of each
+  // sequence {first unit of head 0, shares}
   float* part;
   float* ml;
+  int* info;
   int* count;  // one for each row block of a (sequence, key head), 0 between calls; null: k_attn_join follows
 };
 

@@ -426,6 +426,26 @@ def test_tree_attention_long_context(ctx):
         check(call(ctx, c), c)
 
 
+@pytest.mark.parametrize("tokens,heads", [(1, 2), (3, 40)])
+def test_tree_attention_many_ragged_sequences(ctx, tokens, heads):
+    """More sequences than a wave has lanes, lengths from none to several shares of the work."""
+    g = np.random.default_rng(20)
+    lengths = [int(x) for x in g.integers(0, 40, 70)]
+    lengths[3], lengths[64], lengths[69], lengths[10] = 3000, 1500, 700, -1
+    c = attention_case(ctx, g, lengths, tokens, heads, 2, 64, 8, 16, None)
+    check(call(ctx, c), c)
+
+
+@pytest.mark.parametrize("bits,dim,tokens,heads,kv_heads", [(8, 128, 50, 6, 2), (4, 128, 70, 2, 1), (4, 256, 35, 2, 2),
+                                                            (8, 192, 40, 4, 1), (8, 96, 64, 1, 1), (4, 64, 90, 8, 2)])
+def test_tree_attention_many_rows(ctx, bits, dim, tokens, heads, kv_heads):
+    """49 to 360 rows of a key head, several blocks and shares, a draft that fills whole tiles."""
+    g = np.random.default_rng(21 + dim)
+    c = attention_case(ctx, g, [700, 0, 130], tokens, heads, kv_heads, dim, bits, 32, "tree")
+    check(call(ctx, c), c)
+    assert torch.equal(call(ctx, c), call(ctx, c))
+
+
 def test_tree_attention_offsets_past_32_bits(ctx):
     """A pool of more than 2^32 bytes of codes."""
     pages, heads, dim, page = 17000, 16, 256, 64
