@@ -1389,8 +1389,8 @@ GPTQ_API int gptq_rope(gptq_ctx c, const void* x, int32_t x_type, int64_t tokens
   if (tokens == 0 || heads == 0 || dim == 0) return GPTQ_OK;
   if (!x || !y || (rot > 0 && (!positions || !table || length == 0)))
     return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if (tokens > INT32_MAX || tokens * heads > ((int64_t)1 << 39) / dim)
-    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many values for one launch");
+  if (tokens > INT32_MAX || (int64_t)heads * dim > (1 << 30))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many values");
   // the stride of a dimension of one is never used
   if (tokens == 1) x_token = y_token = 0;
   if (heads == 1) x_head = y_head = 0;

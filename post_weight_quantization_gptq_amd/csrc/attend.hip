@@ -1001,12 +1001,12 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
   const int q4 = p.c.dim >> 2, rows = max(256 / (q4 * G), 1);
   const int i = threadIdx.x / (q4 * G), k = threadIdx.x / q4 % G, d = 4 * (threadIdx.x % q4);
   const int R = p.tokens * p.group;
-  const long long row = (long long)blockIdx.x * rows + i;
-  bool on = i < rows && row < (long long)p.seqs * p.c.heads * R;
+  const unsigned row = blockIdx.x * rows + i;  // (at most 2^30 of them)
+  bool on = i < rows && row < (unsigned)(p.seqs * p.c.heads * R);
   Share me{};
   if (on) {
-    const int bh = (int)(row / R);
-    me = Share{bh / p.c.heads, bh % p.c.heads, 0, p.info[2 * (bh / p.c.heads) + 1], p.info[2 * (bh / p.c.heads)]};
+    const int bh = (int)(row / R), b = bh / p.c.heads;
+    me = Share{b, bh % p.c.heads, 0, p.info[2 * b + 1], p.info[2 * b]};
     on = me.shares > 1;  // a single share has written its result
   }
   join_row<G, false>(p, on, me, (int)(row % R), d, k, &s);

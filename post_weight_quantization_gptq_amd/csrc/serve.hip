@@ -3,6 +3,8 @@
 #include "common.h"
 #include "serve.h"
 
+#include <algorithm>
+
 // Outputs from this size on are stored past the caches: they pass through the
 // eight 4 MB L2 before anyone reads them, and would push the inputs out of the
 // caches behind.  134 MB of values read back: 32 us, 71 with ordinary stores.
@@ -92,12 +94,11 @@ template <class TX, class TY, int V, bool INTER, bool STREAM>
 __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
   const int half = p.rot / 2;
   const int nrot = half / V, nth = nrot + (p.dim - p.rot) / (2 * V);  // threads of one head
-  const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long row = idx / nth;
+  const unsigned idx = blockIdx.x * 256 + threadIdx.x, row = idx / nth;
   const int u = (int)(idx % nth);
-  if (row >= p.tokens * p.heads) return;
-  const long long t = row / p.heads;
-  const int h = (int)(row % p.heads);
+  const long long t = row / (unsigned)p.heads;
+  const int h = (int)(row % (unsigned)p.heads);
+  if (t >= p.tokens) return;
   const TX* x = (const TX*)p.x + t * p.xt + h * p.xh;
   TY* y = (TY*)p.y + t * p.yt + h * p.yh;
   float a[V], b[V], r[V], q[V];
@@ -418,17 +419,26 @@ hipError_t rope_v(const RopeProb& p, hipStream_t st) {
   // 8192 x 40 heads of 128 from float32: 45 us, 53 with four)
   const int v = sizeof(TY) == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
   const int nth = p.dim / (2 * v);
-  const dim3 grid((unsigned)((p.tokens * p.heads * nth + 255) / 256));
   const bool stream = p.tokens * p.heads * p.dim * (long long)sizeof(TY) >= STREAM_BYTES;
-  if (v == 8) {
-    if constexpr (sizeof(TY) == 2)
-      hipLaunchKernelGGL((stream ? k_rope<TX, TY, 8, INTER, true> : k_rope<TX, TY, 8, INTER, false>), grid, dim3(256), 0,
-                         st, p);
-  } else if (v == 4) {
-    hipLaunchKernelGGL((stream ? k_rope<TX, TY, 4, INTER, true> : k_rope<TX, TY, 4, INTER, false>), grid, dim3(256), 0,
-                       st, p);
-  } else {
-    hipLaunchKernelGGL((k_rope<TX, TY, 1, INTER, false>), grid, dim3(256), 0, st, p);
+  // threads of a launch are counted in 32 bits
+  const long long most = std::max((1LL << 31) / ((long long)p.heads * nth), 1LL);
+  for (long long t = 0; t < p.tokens; t += most) {
+    RopeProb q = p;
+    q.tokens = std::min(most, p.tokens - t);
+    q.x = (const TX*)p.x + t * p.xt;
+    q.y = (TY*)p.y + t * p.yt;
+    q.pos = p.pos + t;
+    const dim3 grid((unsigned)((q.tokens * q.heads * nth + 255) / 256));
+    if (v == 8) {
+      if constexpr (sizeof(TY) == 2)
+        hipLaunchKernelGGL((stream ? k_rope<TX, TY, 8, INTER, true> : k_rope<TX, TY, 8, INTER, false>), grid, dim3(256),
+                           0, st, q);
+    } else if (v == 4) {
+      hipLaunchKernelGGL((stream ? k_rope<TX, TY, 4, INTER, true> : k_rope<TX, TY, 4, INTER, false>), grid, dim3(256), 0,
+                         st, q);
+    } else {
+      hipLaunchKernelGGL((k_rope<TX, TY, 1, INTER, false>), grid, dim3(256), 0, st, q);
+    }
   }
   return hipGetLastError();
 }
