@@ -352,7 +352,9 @@ int gptq_gemm_wqa16(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, con
 /* Serving operators: what a layer runs between its quantised products when it
  * answers token by token.  (The pages stop at the quantised weights' matrix
  * products; these operators have no counterpart there.)  All ASYNC on the
- * context's stream; device buffers, caller-owned.  Element types of x, y, K
+ * context's stream; device buffers, caller-owned.  They may be captured into
+ * a HIP graph: the attention needs workspace, which its first call of a size
+ * allocates, so run a call once before it is captured.  Element types of x, y, K
  * and V: GPTQ_BF16 (bit patterns) or GPTQ_F32; their last dimension (the head)
  * is contiguous, the strides of tokens and heads are given in elements. */
 #define GPTQ_BF16 0
@@ -464,7 +466,7 @@ int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t
  * deployable outputs k_pack, k_unpack, k_lr_quant, k_gemm_w4a16,
  * k_gemv_w4a16 (4-bit codes), k_gemm_wqa16, k_gemv_wqa16 (other widths), and
  * for the serving operators k_rope_table, k_rope, k_kv_write, k_kv_read,
- * k_tree_attn.
+ * k_tree_attn, k_tree_attn_wide, k_attn_join.
  * gptq_kernel_time
  * waits for the recorded events and returns the summed elapsed milliseconds
  * and the number of timed launches of kernel `name` (0 and 0 if none).  Each

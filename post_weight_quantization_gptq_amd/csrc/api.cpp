@@ -38,6 +38,7 @@ struct gptq_ctx_s {
   int nxcd = 8;
   std::string err;
   DevBuf partials, xt, facA, facY, work, eblk, objp, dinv, slots, blob, lora, r2d, qr, attn, counts;
+  std::vector<void*> outgrown;  // see ensure_kept
   void* hblob = nullptr;  // pinned staging for the task tables
   size_t hblob_cap = 0;
   void* hsmall = nullptr;  // pinned read-back area
@@ -159,6 +160,19 @@ int ensure(gptq_ctx c, DevBuf& b, size_t bytes) {
     return set_err(c, GPTQ_ERR_NO_MEMORY, "device allocation of %zu bytes failed", want);
   }
   b.cap = want;
+  return GPTQ_OK;
+}
+
+// ensure() for buffers of calls that may be captured: an outgrown one is kept
+// until the context goes, since a graph captured with it may be replayed.  It
+// doubles, so that all of them take at most twice the last one.
+int ensure_kept(gptq_ctx c, DevBuf& b, size_t bytes) {
+  if (b.cap >= bytes && b.p) return GPTQ_OK;
+  DevBuf next;
+  const int rc = ensure(c, next, std::max(bytes, 2 * b.cap));
+  if (rc) return rc;
+  if (b.p) c->outgrown.push_back(b.p);
+  b = next;
   return GPTQ_OK;
 }
 
@@ -663,6 +677,7 @@ GPTQ_API int gptq_destroy(gptq_ctx c) {
                       &c->objp, &c->slots, &c->blob, &c->lora, &c->r2d, &c->qr, &c->attn, &c->counts};
     for (DevBuf* b : bufs)
       if (b->p) (void)hipFree(b->p);
+    for (void* q : c->outgrown) (void)hipFree(q);
     if (c->hblob) (void)hipHostFree(c->hblob);
     if (c->hsmall) (void)hipHostFree(c->hsmall);
     if (c->blob_ev) (void)hipEventDestroy(c->blob_ev);
@@ -1546,14 +1561,14 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   const bool split = p.most > 1, fuse = split && p.shares <= 8 && p.nb == 1 && !p.wide;
   {
     const size_t rows = split ? (size_t)p.kept * tokens * p.group : 0;
-    if ((rc = ensure(c, c->attn, (rows * (cache->dim + 2) + 2 * (size_t)seqs) * sizeof(float)))) return rc;
+    if ((rc = ensure_kept(c, c->attn, (rows * (cache->dim + 2) + 2 * (size_t)seqs) * sizeof(float)))) return rc;
     p.part = (float*)c->attn.p;
     p.ml = p.part + rows * cache->dim;
     p.info = (int*)(p.ml + 2 * rows);
   }
   if (fuse) {
     const size_t had = c->counts.cap;
-    if ((rc = ensure(c, c->counts, (size_t)seqs * cache->heads * p.nrb * sizeof(int)))) return rc;
+    if ((rc = ensure_kept(c, c->counts, (size_t)seqs * cache->heads * p.nrb * sizeof(int)))) return rc;
     if (c->counts.cap != had)
       HIPCHK(c, launch_zero_f32((float*)c->counts.p, (long long)(c->counts.cap / sizeof(float)), c->stream));
     p.count = (int*)c->counts.p;

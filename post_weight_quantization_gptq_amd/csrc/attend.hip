@@ -113,8 +113,8 @@ struct Span {
   int b, len, npos;
 };
 __device__ __forceinline__ Span span_of(const AttnProb& p, int b) {
-  const int len = p.lengths[b], cap = p.width << p.c.pshift;
-  return Span{b, len, len < 0 ? 0 : (int)min((long long)len + p.tokens, (long long)cap)};
+  const int cap = p.width << p.c.pshift, len = min(p.lengths[b], cap);  // (cap is at most 2^29)
+  return Span{b, len, len < 0 ? 0 : min(len + p.tokens, cap)};
 }
 // A workgroup's share of the work: the positions of sequence b, key head h, are
 // cut into `shares` runs of tiles of nearly the same number, this is run

@@ -385,6 +385,39 @@ def test_tree_attention_short_tables_and_bad_pages(ctx, tokens):
     assert not bool(call(ctx, c).any())
 
 
+def test_tree_attention_lengths_past_the_table(ctx):
+    """The largest length there is: every position of the table is before the drafted tokens."""
+    g = np.random.default_rng(22)
+    c = attention_case(ctx, g, [150, 60], 2, 4, 2, 64, 8, 16, None)
+    c["tables"] = c["tables"][:, :2].copy()
+    c["lengths"] = np.array([2 ** 31 - 1, 2 ** 31 - 2], np.int32)
+    check(call(ctx, c), c)
+
+
+def test_graph_outlives_a_larger_call():
+    """A captured call keeps its workspace when a later one needs more."""
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ctx = Context("cuda:0")
+        g = np.random.default_rng(23)
+        small = attention_case(ctx, g, [2000], 4, 8, 1, 64, 8, 64, None)
+        t, n = i32(small["tables"]), i32(small["lengths"])
+        want = ctx.tree_attention(small["q"], small["cache"], t, n)
+        graph = torch.cuda.CUDAGraph()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            out = ctx.tree_attention(small["q"], small["cache"], t, n)
+        large = attention_case(ctx, g, [3000, 2500], 60, 16, 2, 128, 8, 64, None)
+        for _ in range(3):
+            call(ctx, large)
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(out, want)
+            out.zero_()
+        del graph
+        ctx.close()
+
+
 def test_tree_attention_strided_queries_and_output(ctx):
     g = np.random.default_rng(14)
     c = attention_case(ctx, g, [50, 60], 3, 8, 2, 96, 4, 32, None)
