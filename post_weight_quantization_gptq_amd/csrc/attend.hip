@@ -61,6 +61,18 @@ __device__ __forceinline__ float sum_groups(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// A value that is the same in all lanes, as such.
+__device__ __forceinline__ size_t uniform(size_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (size_t)hi << 32 | lo;
+}
+// Entry of a table that nothing writes during the launch, at an address that is
+// the same in all lanes: read through the scalar cache.
+__device__ __forceinline__ int scalar_load(const int* p) {
+  typedef const __attribute__((address_space(4))) int cint;
+  return *(cint*)uniform((size_t)p);
+}
 // A load that asks the caches not to keep what is read once (32 contexts of
 // 8192 tokens: 83.4 against 85.7 us; where blocks share the codes it costs: 108
 // rows of 4000 positions 48 against 45 us).
@@ -555,30 +567,46 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
 
   const int pm = (1 << c.pshift) - 1, lastchunk = max(npos - 1, 0) / CH;
   const int* table = p.tables + (size_t)b * p.width;
-  // page of a chunk (of the last one there is for those past the end)
-  auto page_of = [&](int chunk, bool& bad) {
-    const int pg = glb(table)[(min(chunk, lastchunk) * CH) >> c.pshift];
-    bad = (unsigned)pg >= (unsigned)c.pages;
-    return bad ? 0 : pg;
-  };
-  // (page, head) block and offset in it of the chunks of a tile that the lane
-  // reads: of its key rows, of its scores and values
+  // A tile that lies in one page (pages of TP positions or more) is found by one
+  // scalar load, and its addresses are scalar but for a constant of the lane;
+  // otherwise every lane looks up the pages of the two chunks that it reads, of
+  // its key rows and of its scores and values (the last chunk there is for those
+  // past the end).
+  const bool one = (1 << c.pshift) >= TP;
   struct Place {
     int k, v, ok, ov;
     bool bad;
   };
+  auto inside = [&](int pg) { return (unsigned)pg < (unsigned)c.pages; };
   auto find = [&](int tl) {
     Place q;
-    bool bk;
-    q.k = page_of(4 * tl + (n >> 2), bk);
-    q.v = page_of(4 * tl + g, q.bad);
-    q.ok = (min(4 * tl + (n >> 2), lastchunk) * CH) & pm;
-    q.ov = (min(4 * tl + g, lastchunk) * CH) & pm;
+    if (one) {
+      const int at = min(tl * TP, max(npos - 1, 0)), pg = scalar_load(table + (at >> c.pshift));
+      q.bad = !inside(pg);
+      q.k = q.v = q.bad ? 0 : pg;
+      q.ok = q.ov = tl * TP & pm;
+    } else {
+      const int ck = min(4 * tl + (n >> 2), lastchunk) * CH, cv = min(4 * tl + g, lastchunk) * CH;
+      const int pk = glb(table)[ck >> c.pshift], pv = glb(table)[cv >> c.pshift];
+      q.bad = !inside(pv);
+      q.k = inside(pk) ? pk : 0;
+      q.v = q.bad ? 0 : pv;
+      q.ok = ck & pm;
+      q.ov = cv & pm;
+    }
     return q;
   };
+  // slot of the chunk's first position, counted over all heads: of the tile (one
+  // page; uniform) and the lane's chunk in it, or of the lane's chunk
+  auto slot = [&](int pg, int off, int chunk, size_t& base) {
+    base = (((size_t)pg * c.heads + h) << c.pshift) + off;
+    if (one) base = uniform(base);
+    return one ? CH * chunk : 0;
+  };
   auto load_k = [&](T& t, const Place& q) {
-    const size_t at = (((size_t)q.k * c.heads + h) << c.pshift) + q.ok;
-    const uint8_t* kr = c.kc + (at + (n & 3)) * T::RB;
+    size_t at;
+    const int in = slot(q.k, q.ok, n >> 2, at);
+    const uint8_t* kr = c.kc + at * T::RB + (in + (n & 3)) * T::RB;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const uint8_t* r = kr + 4 * i * T::RB;
@@ -595,20 +623,22 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       }
       if constexpr (T::R16) t.k[i][T::NW - 1] = *glb((const uint32_t*)(r + T::RB - 16 + 4 * g));
     }
-    t.kz = *glb((const Chunk*)(c.kz + at));
+    t.kz = *glb((const Chunk*)(c.kz + at + in));
   };
   auto load_g = [&](T& t, const Place& q) {
     t.bad = q.bad;
-    const size_t at = (((size_t)q.v * c.heads + h) << c.pshift) + q.ov;
+    size_t at;
+    const int in = slot(q.v, q.ov, g, at);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      t.ks[i] = *glb((const f32x4*)(c.ks + at + 4 * i));
-      t.vs[i] = *glb((const f32x4*)(c.vs + at + 4 * i));
+      t.ks[i] = *glb((const f32x4*)(c.ks + at + in + 4 * i));
+      t.vs[i] = *glb((const f32x4*)(c.vs + at + in + 4 * i));
     }
-    t.vz = *glb((const Chunk*)(c.vz + at));
+    t.vz = *glb((const Chunk*)(c.vz + at + in));
   };
   auto load_v = [&](T& t, const Place& q) {
-    const uint8_t* vr = c.vc + ((((size_t)q.v * c.heads + h) * T::RB + n) << c.pshift) + q.ov;
+    const size_t blk = (((size_t)q.v * c.heads + h) * T::RB << c.pshift) + q.ov;
+    const uint8_t* vr = c.vc + (one ? uniform(blk) : blk) + (n << c.pshift) + (one ? CH * g : 0);
 #pragma unroll
     for (int i = 0; i < NMB; ++i) t.v[i] = fetch<ONCE>((const Chunk*)(vr + ((size_t)(16 * i) << c.pshift)));
   };
