@@ -416,9 +416,10 @@ typedef struct {
 
 /* Quantise K[tokens][heads][dim] and V into the cache: token t goes to
  * slots[t] (a slot outside the pool: the token is skipped; the same slot
- * twice in one call: undefined contents).  Per row v, in fp32 steps as
- * gptq_quantize_lowrank: lo = min(min v, 0), hi = max(max v, 0), s = (hi - lo)
- * / maxq, r = 1/s, z = clamp(rne(-lo r)), q = clamp(rne(fl32(fl32(v r) + z))).
+ * twice in one call: undefined contents).  Per row v, in fp32 steps: lo = min(min v,
+ * 0), hi = max(max v, 0), s = fl32(hi - lo) fl32(1/maxq), r = 1/s, z = clamp(rne(-lo
+ * r)), q = clamp(rne(fl32(fl32(v r) + z))), as gptq_quantize_lowrank but for the
+ * product with 1/maxq in place of its quotient (one rounding of s apart).
  * A range below 2^-100 is stored as zeros (s = 1); a row with a non-finite
  * value, or whose range overflows, reads back as NaN.  Rows aligned to four
  * values (else GPTQ_ERR_UNSUPPORTED). */

@@ -74,7 +74,7 @@ def kv_grid(row, bits):
             return F(np.nan), 0, np.zeros(row.shape, np.uint8)
         if span < F(2.0 ** -100):
             return F(1), 0, np.zeros(row.shape, np.uint8)
-        s = F(span / maxq)
+        s = F(span * F(F(1) / maxq))
         r = F(F(1) / s)
         z = min(max(np.rint(F(-lo * r)), F(0)), maxq)
         x = (row * r).astype(F)

@@ -159,14 +159,14 @@ __device__ __forceinline__ int ceil_div(int a, int b) {
   return q;
 }
 // Workgroups go to sequences by their lengths, which only the device knows:
-// the fewest tiles for each, at least 256 positions, such that no more of them
-// (p.fit for a key head and row block) are made than run at once.  The longest
+// the fewest tiles for each, at least LEAST, such that no more of them (p.fit for
+// a key head and row block) are made than run at once.  The longest
 // share is what a call takes: eight trees over 0 to 4093 positions 43 us, 47
 // with equally many shares for each sequence.  The whole wave takes part.
-template <int TP>
+template <int TP, int LEAST>
 __device__ __forceinline__ bool find_share(const AttnProb& p, int unit, Share& o) {
+  static_assert(LEAST * TP >= 256, "the host's bounds count shares of 256 positions or more");
   const int lane = threadIdx.x & 63, H = p.c.heads, fit = p.fit;
-  constexpr int LEAST = 256 / TP;
   auto tiles = [&](int b) { return b < p.seqs ? (span_of(p, b).npos + TP - 1) / TP : 0; };
   if (p.seqs == 1) {
     const int t = tiles(0);
@@ -524,7 +524,7 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 // invisible positions are taken out of scores and weights by selection,
 // whatever their scales hold.
 //
-// The four waves of a workgroup take every fourth tile of its share of the
+// The WV waves of a workgroup take every WV-th tile of its share of the
 // positions and are joined in LDS in a fixed order; of several shares
 // the unnormalised rows go to the workspace.  The shares of a row are
 // joined, in their order, by the workgroup that comes last (p.count, which it
@@ -536,17 +536,17 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 // rows by its vector instructions, about ten for a score and two for a code: 40
 // rows of 131071 positions, 4 heads at 4 bits, 40 us, issued 55% of the time;
 // 32 positions a tile, so that two waves fit a SIMD without spills.
-template <int DIM, int BITS, int NB, int TP, int OCC>
-__global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
+template <int DIM, int BITS, int NB, int TP, int WV, int OCC>
+__global__ __launch_bounds__(64 * WV, OCC) void k_tree_attn(const AttnProb p) {
   typedef Tile<DIM, BITS, TP> T;
   typedef typename T::Chunk Chunk;
   constexpr int CH = T::CH, NI = T::NI, NS = T::NS;
   constexpr int NK = DIM / 32, NO = DIM / 16, NMB = T::NMB;
   constexpr bool ONCE = NB == 1;  // up to 16 rows: one block, so that the codes are read once
-  __shared__ float sm[4][16 * NB], sl[4][16 * NB], scq[16 * NB];
+  __shared__ float sm[WV][16 * NB], sl[WV][16 * NB], scq[16 * NB];
   __shared__ union {
     u32x4 q[NB][NK][64];
-    f32x4 o[2][NB * NO][64];
+    f32x4 o[WV / 2][NB * NO][64];
   } sh;
   const KvPool& c = p.c;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   const int x = blockIdx.x / (8 * p.nrb), rem = blockIdx.x % (8 * p.nrb);
   const int rb = rem >> 3, unit = 8 * x + (rem & 7);
   Share me;
-  if (!find_share<TP>(p, unit, me)) return;
+  if (!find_share<TP, (WV * TP > 256 ? WV : 256 / TP)>(p, unit, me)) return;
   const int b = __builtin_amdgcn_readfirstlane(me.b), h = __builtin_amdgcn_readfirstlane(me.h);
   const int split = __builtin_amdgcn_readfirstlane(me.split), shares = __builtin_amdgcn_readfirstlane(me.shares);
   if (h == 0 && split == 0 && rb == 0 && tid == 0) {  // for the join
@@ -662,7 +662,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
 
   // queries: row n of block nb, in the order of the key codes' words
 #pragma unroll 1
-  for (int nb = w; nb < NB; nb += 4) {
+  for (int nb = w; nb < NB; nb += WV) {
     u32x4 q[NK];
     const float f = query_row<NK, BITS>(
         p, b, h, 16 * (NB * rb + nb) + n,
@@ -745,9 +745,9 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
 
   // A part of the next tile is asked for as soon as this tile's has been used.
   if (work) {
-    at = find(tile + 4);
+    at = find(tile + WV);
     while (true) {
-      const bool more = tile + 4 < t1;
+      const bool more = tile + WV < t1;
       scores(t);
       __builtin_amdgcn_sched_barrier(0);
       if (more) load_k(t, at);
@@ -763,8 +763,8 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
       __builtin_amdgcn_sched_barrier(0);
       if (!more) break;
       load_v(t, at);
-      tile += 4;
-      at = find(tile + 4);
+      tile += WV;
+      at = find(tile + WV);
     }
   }
 
@@ -781,10 +781,10 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   for (int nb = 0; nb < NB; ++nb) {
     float mx = -INFINITY, s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, sm[k][16 * nb + n]);
+    for (int k = 0; k < WV; ++k) mx = fmaxf(mx, sm[k][16 * nb + n]);
     const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s += sl[k][16 * nb + n] * __builtin_amdgcn_exp2f(sm[k][16 * nb + n] - ref);
+    for (int k = 0; k < WV; ++k) s += sl[k][16 * nb + n] * __builtin_amdgcn_exp2f(sm[k][16 * nb + n] - ref);
     const float f = __builtin_amdgcn_exp2f(r.M[nb] - ref);
 #pragma unroll
     for (int i = 0; i < NO; ++i) r.acc[nb][i] *= f;
@@ -799,16 +799,14 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
 #pragma unroll
     for (int i = 0; i < NB * NO; ++i) r.acc[i / NO][i % NO] += sh.o[k][i][lane];
   };
-  if (w >= 2) put(w - 2);
-  __syncthreads();
-  if (w < 2) add(w);
-  __syncthreads();
-  if (w == 1) put(0);
-  __syncthreads();
-  if (w == 0) {
-    add(0);
-    put_rows(p, r, me, 16 * NB * rb);
+#pragma unroll
+  for (int half = WV / 2; half > 0; half /= 2) {
+    if (w >= half && w < 2 * half) put(w - half);
+    __syncthreads();
+    if (w < half) add(w);
+    __syncthreads();
   }
+  if (w == 0) put_rows(p, r, me, 16 * NB * rb);
   if (!p.count || shares == 1) return;
   __shared__ int last;
   if (w == 0) {
@@ -823,7 +821,7 @@ __global__ __launch_bounds__(256, OCC) void k_tree_attn(const AttnProb p) {
   __syncthreads();
   if (!last) return;
   const int r1 = min(16 * NB, R - 16 * NB * rb);
-  for (int i = tid; i < r1 * (DIM / 4); i += 256)
+  for (int i = tid; i < r1 * (DIM / 4); i += 64 * WV)
     join_row<1, true>(p, true, me, 16 * NB * rb + i / (DIM / 4), 4 * (i % (DIM / 4)), 0, nullptr);
 }
 
@@ -858,7 +856,7 @@ __global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
   const int x = blockIdx.x / (8 * p.nrb), rem = blockIdx.x % (8 * p.nrb);
   const int rb = rem >> 3, unit = 8 * x + (rem & 7);
   Share me;
-  if (!find_share<TP>(p, unit, me)) return;
+  if (!find_share<TP, 256 / TP>(p, unit, me)) return;
   const int b = __builtin_amdgcn_readfirstlane(me.b), h = __builtin_amdgcn_readfirstlane(me.h);
   const int split = __builtin_amdgcn_readfirstlane(me.split), shares = __builtin_amdgcn_readfirstlane(me.shares);
   if (h == 0 && split == 0 && rb == 0 && tid == 0) {  // for the join
@@ -1073,8 +1071,12 @@ void plan_tree_attn(AttnProb& p, int ncu) {
   }
   // shares of one head and row block: what runs at once, and one more for each
   // sequence by rounding up; those of sequences with more than one are at most
-  // twice what runs at once, or, at 256 positions each, what the tables hold
-  const long long slots = (p.c.dim > 128 && !p.wide && p.nb == 2 ? 1 : 2) * ncu;
+  // twice what runs at once, or, at 256 positions or more each, what the tables hold
+  // Workgroups of four waves, two to a CU; from 17 rows on of eight (head sizes
+  // up to 128), or of four that need a SIMD's registers each, one to a CU: their
+  // shares are half as many to join (40 rows of 131071 positions 41 us, 46 with
+  // four waves; 4 rows of 4096 to 8192 positions 89 us with eight, 85 with four).
+  const long long slots = (p.wide || p.nb == 1 ? 2 : 1) * ncu;
   const long long fit = std::max(slots / ((long long)p.c.heads * p.nrb), 1LL);
   p.fit = (int)fit;
   const long long hold = (((long long)p.width << p.c.pshift) + 255) / 256;
@@ -1093,12 +1095,16 @@ void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
       hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 1, TP>), grid, dim3(256), 0, st, p);
     else if constexpr (DIM <= 128)
       hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 2, TP>), grid, dim3(256), 0, st, p);
-  } else if (p.nb == 1)
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, TP, 2>), grid, dim3(256), 0, st, p);
-  else if (p.nb == 2)
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, DIM <= 128 ? 2 : 1>), grid, dim3(256), 0, st, p);
-  else if constexpr (DIM <= 128)
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 3, 32, 2>), grid, dim3(256), 0, st, p);
+  } else if (p.nb == 1) {
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, TP, 4, 2>), grid, dim3(256), 0, st, p);
+  } else if (p.nb == 2) {
+    if constexpr (DIM <= 128)
+      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 8, 2>), grid, dim3(512), 0, st, p);
+    else
+      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 4, 1>), grid, dim3(256), 0, st, p);
+  } else if constexpr (DIM <= 128) {
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 3, 32, 8, 2>), grid, dim3(512), 0, st, p);
+  }
 }
 template <int BITS>
 hipError_t attn_dim(const AttnProb& p, hipStream_t st) {

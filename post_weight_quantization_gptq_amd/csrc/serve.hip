@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
 
 // ----------------------------------------------------------- cache write --
 // Grid of one row (the dim values of a token's K or V in one head), every
-// step in fp32: lo = min(v, 0), hi = max(v, 0), s = (hi - lo) / maxq,
+// step in fp32: lo = min(v, 0), hi = max(v, 0), s = (hi - lo) fl32(1 / maxq),
 // r = 1 / s, z = rne(-lo r).  A range under 2^-100 (r would overflow) is
 // stored as zeros on s = 1; a row with a NaN or an infinity, or whose range
 // overflows, gets s = NaN and so reads back as NaN.
@@ -169,7 +169,7 @@ __device__ __forceinline__ KvGrid kv_grid(float mn, float mx, bool bad, float ma
     g.r = 1.f;
     g.z = 0.f;
   } else {
-    g.s = d / maxq;
+    g.s = __fmul_rn(d, 1.f / maxq);
     g.r = 1.f / g.s;
     g.z = fminf(fmaxf(rintf(__fmul_rn(-lo, g.r)), 0.f), maxq);
   }
