@@ -534,7 +534,7 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 // tokens, 8 heads of 128 at 8 bits, 423 MB in 85 us, 5.0 TB/s, what a large copy
 // moves; 64 positions a tile, so that 17 KB a wave are on their way.  With more
 // rows by its vector instructions, about ten for a score and two for a code: 40
-// rows of 131071 positions, 4 heads at 4 bits, 40 us, issued 55% of the time;
+// rows of 131071 positions, 4 heads at 4 bits, 38 us, issued 55% of the time;
 // 32 positions a tile, so that two waves fit a SIMD without spills.
 template <int DIM, int BITS, int NB, int TP, int WV, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void k_tree_attn(const AttnProb p) {
@@ -1034,7 +1034,7 @@ __global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
 
 // The shares of every row, where a launch of its own joins them: bound by
 // reading them (13824 rows of up to 11 shares of 128 dimensions 7.8 us, 7 TB/s
-// from the last-level cache) or by its latency (160 rows of 128 shares 9.3 us).
+// from the last-level cache) or by its latency (160 rows of 64 shares 5.6 us).
 template <int G>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
   __shared__ JoinLds<G> s;
