@@ -12,6 +12,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 namespace {
 
@@ -41,11 +42,18 @@ __device__ __forceinline__ uint32_t diff_bf16(uint32_t c, uint32_t z) {
   asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[1,0,1] op_sel_hi:[1,0,1]" : "=v"(hi) : "v"(c), "v"(z));
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
-// the leading 16 bits of two floats (their bfloat16 truncations), and those of what the truncation left
-__device__ __forceinline__ uint32_t lead16(float a, float b) {
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+// Two floats as the sum of two bfloat16 pairs: each to the nearest (ties to
+// even), then what that left (exact in float32) to the nearest.  As many
+// instructions as cutting both off, which would leave every weight, and so every
+// result, too small by 2^-17 on average.
+__device__ __forceinline__ uint32_t near16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
-__device__ __forceinline__ float rest16(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
+__device__ __forceinline__ void split16(float a, float b, uint32_t& lead, uint32_t& next) {
+  lead = near16(a, b);
+  next = near16(a - __uint_as_float(lead << 16), b - __uint_as_float(lead & 0xFFFF0000u));
+}
 
 // largest value (sum) of the four lanes that differ in lane / 16
 __device__ __forceinline__ float max_groups(float v) {
@@ -375,8 +383,10 @@ __device__ __forceinline__ void weigh(Rows<NB, NO>& r, int nb, const f32x4* S, c
       // 4 bits: positions (0, 2), (1, 3) of every four, as their bytes come apart
       const float a = xs[8 * s + (BITS == 8 ? 2 * j : 4 * (j >> 1) + (j & 1))];
       const float b = xs[8 * s + (BITS == 8 ? 2 * j + 1 : 4 * (j >> 1) + (j & 1) + 2)];
-      P[0][s][j] = lead16(a, b);
-      P[1][s][j] = lead16(rest16(a), rest16(b));
+      uint32_t lead, next;
+      split16(a, b, lead, next);
+      P[0][s][j] = lead;
+      P[1][s][j] = next;
     }
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -515,8 +525,9 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 // they wait in LDS in operand order.
 //
 // Weights enter the second product times their position's scale, as two
-// bfloat16 numbers, the leading 8 bits and the next 8: with one of them the
-// weights' rounding would be as large as the result's, and float16's range
+// bfloat16 numbers, the nearest to it and the nearest to what is left, within 2^-16
+// of it and without a bias: with one of them the weights' rounding would be as large
+// as the result's, and float16's range
 // would lose the weights under 2^-29 of the largest, which are all there is
 // where the others' values are zero.
 //

@@ -1,0 +1,37 @@
+"""Serving operators on the GPU where a rounding, a size or a setting decides the result."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from post_weight_quantization_gptq_amd import Context  # noqa: E402
+from test_gpu_serving import attention_case, call, i32  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    c = Context("cuda:0")
+    yield c
+    c.close()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens,heads,kv_heads", [(1, 4, 1), (5, 8, 1), (32, 2, 1), (60, 4, 2)])
+def test_weights_have_no_bias(ctx, bits, tokens, heads, kv_heads):
+    """Values that are all the same number, 2^-18 of it above the middle of two bfloat16 numbers, come out as the upper one.
+
+    The result is that number whatever the weights.  About a thousand positions take part with weights of one size, so
+    that parts rounded to nearest (each weight within 2^-16, 2^-18.6 rms) leave an error near 2^-23 and float32 sums one
+    near 2^-21; parts cut off leave every weight and the result too small by 2^-17.
+    """
+    g = np.random.default_rng(30 + bits + tokens)
+    c = attention_case(ctx, g, [1000, 900], tokens, heads, kv_heads, 64, bits, 32, None, sharp=0.2)
+    value = np.float32((1 + 2.0 ** -8) * (1 + 2.0 ** -18))
+    cache = c["cache"]
+    cache.v_codes.fill_(0x11 if bits == 4 else 1)
+    cache.v_zeros.zero_()
+    cache.v_scales.fill_(float(value))
+    got = call(ctx, c).float()
+    assert bool((got == 1 + 2.0 ** -7).all()), "%d of %d results on the lower side" % (int((got < 1.005).sum()), got.numel())
