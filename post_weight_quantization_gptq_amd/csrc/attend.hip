@@ -1049,52 +1049,22 @@ __global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
 template <int G>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
   __shared__ JoinLds<G> s;
-  const int q4 = p.c.dim >> 2, rows = max(256 / (q4 * G), 1);
-  const int i = threadIdx.x / (q4 * G), k = threadIdx.x / q4 % G, d = 4 * (threadIdx.x % q4);
-  const int R = p.tokens * p.group;
-  const unsigned row = blockIdx.x * rows + i;  // (at most 2^30 of them)
-  bool on = i < rows && row < (unsigned)(p.seqs * p.c.heads * R);
+  const JoinThread t = join_thread(threadIdx.x, p.c.dim, G);
+  const int rows = blockDim.x / (p.c.dim / 4 * G), R = p.tokens * p.group;
+  const unsigned row = blockIdx.x * rows + t.i;  // (at most 2^30 of them)
+  bool on = row < (unsigned)(p.seqs * p.c.heads * R);
   Share me{};
   if (on) {
     const int bh = (int)(row / R), b = bh / p.c.heads;
     me = Share{b, bh % p.c.heads, 0, p.info[2 * b + 1], p.info[2 * b]};
     on = me.shares > 1;  // a single share has written its result
   }
-  join_row<G, false>(p, on, me, (int)(row % R), d, k, &s);
+  join_row<G, false>(p, on, me, (int)(row % R), t.d, t.k, &s);
 }
 
-// Rows of a call, and shares of its positions.  k_tree_attn takes as few blocks
-// of up to 48 rows (32 for head sizes above 128, whose sums need the registers)
-// as hold the rows of a (sequence, key head), of equal size; where that is more
-// than one, k_tree_attn_wide takes 64 or 128 rows a block if it pads them to no
-// more.  24 sequences of 8 heads, 2048 to 4096 positions of 128, 8 bits, narrow
-// and wide: 64 rows 84.0 and 76.5 us, 96 rows 101.5 and 105.1, 128 rows 136.4
-// and 115.2, 192 rows 181.4 and 207.6, 256 rows 229.9 and 218.3.
 void plan_tree_attn(AttnProb& p, int ncu) {
-  const long long R = (long long)p.tokens * p.group, r16 = (R + 15) / 16, most = p.c.dim <= 128 ? 3 : 2;
-  p.nrb = (int)((r16 + most - 1) / most);
-  p.nb = (int)((r16 + p.nrb - 1) / p.nrb);
-  const long long wide = R > 64 && p.c.dim <= 128 ? 8 : 4, wrb = (r16 + wide - 1) / wide;
-  p.wide = p.nrb > 1 && wrb * wide <= (long long)p.nrb * p.nb;
-  if (p.wide) {
-    p.nrb = (int)wrb;
-    p.nb = (int)wide / 4;
-  }
-  // shares of one head and row block: what runs at once, and one more for each
-  // sequence by rounding up; those of sequences with more than one are at most
-  // twice what runs at once, or, at 256 positions or more each, what the tables hold
-  // Workgroups of four waves, two to a CU; from 17 rows on of eight (head sizes
-  // up to 128), or of four that need a SIMD's registers each, one to a CU: their
-  // shares are half as many to join (40 rows of 131071 positions 41 us, 46 with
-  // four waves; 4 rows of 4096 to 8192 positions 89 us with eight, 85 with four).
-  const long long slots = (p.wide || p.nb == 1 ? 2 : 1) * ncu;
-  const long long fit = std::max(slots / ((long long)p.c.heads * p.nrb), 1LL);
-  p.fit = (int)fit;
   const long long hold = (((long long)p.width << p.c.pshift) + 255) / 256;
-  p.units = (int)((std::min(fit, hold * p.seqs) + p.seqs) * p.c.heads);
-  p.kept = (int)(std::min(2 * fit, hold * p.seqs) * p.c.heads);
-  p.most = (int)std::min(fit, hold);
-  p.shares = (int)std::min(hold, std::max(fit / p.seqs, 1LL));
+  (AttnPlan&)p = plan_attention((long long)p.tokens * p.group, p.seqs, p.c.heads, p.c.dim, hold, ncu);
 }
 
 namespace {
@@ -1136,17 +1106,14 @@ hipError_t launch_tree_attn(const AttnProb& p, int bits, hipStream_t st) {
 }
 
 hipError_t launch_attn_join(const AttnProb& p, hipStream_t st) {
-  // eight threads for a value where there are many shares: 160 rows of 128
-  // shares 8 us, 15 with one; 13824 rows of three shares 5 us, 11 with eight
-  const int G = p.shares >= 16 ? (p.c.dim <= 128 ? 8 : 4) : 1;
-  const int rows = std::max(256 / (p.c.dim / 4 * G), 1);
+  const JoinPlan j = plan_join(p.c.dim, p.shares);
   const long long n = (long long)p.seqs * p.c.heads * p.tokens * p.group;
-  const dim3 grid((unsigned)((n + rows - 1) / rows));
-  if (G == 8)
-    hipLaunchKernelGGL(k_attn_join<8>, grid, dim3(256), 0, st, p);
-  else if (G == 4)
-    hipLaunchKernelGGL(k_attn_join<4>, grid, dim3(256), 0, st, p);
+  const dim3 grid((unsigned)((n + j.rows - 1) / j.rows)), block(j.threads);
+  if (j.G == 8)
+    hipLaunchKernelGGL(k_attn_join<8>, grid, block, 0, st, p);
+  else if (j.G == 4)
+    hipLaunchKernelGGL(k_attn_join<4>, grid, block, 0, st, p);
   else
-    hipLaunchKernelGGL(k_attn_join<1>, grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL(k_attn_join<1>, grid, block, 0, st, p);
   return hipGetLastError();
 }

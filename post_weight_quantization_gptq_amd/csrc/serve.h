@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attend_plan.h"
+
 // One rotary call.  Strides count elements; table is [length][2][rot / 2].
 struct RopeProb {
   const void* x;
@@ -53,7 +55,7 @@ struct KvReadProb {
 };
 
 // Attention of seqs x tokens query tokens over the cache.
-struct AttnProb {
+struct AttnProb : AttnPlan {
   KvPool c;
   const uint16_t* q;  // bf16 bits
   uint16_t* o;
@@ -64,11 +66,6 @@ struct AttnProb {
   int seqs, tokens, heads, group;  // group = heads / c.heads
   int width, words;
   float scale;  // of the scores, times log2(e)
-  // Plan: row blocks of 16 nb rows (64 nb in the kernel for many rows), shares
-  // of a key head and row block that run at once, the most units (shares of a key
-  // head) there can be, the most of them in the workspace, and the most shares
-  // and the expected number of a sequence.
-  int nb, nrb, wide, fit, units, kept, most, shares;
   // workspace: unnormalised rows [unit][row][dim] with their {M, l}, and of each
   // sequence {first unit of head 0, shares}
   float* part;

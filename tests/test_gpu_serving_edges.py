@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from post_weight_quantization_gptq_amd import Context  # noqa: E402
-from test_gpu_serving import attention_case, call, i32  # noqa: E402
+from test_gpu_serving import attention_case, call, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,24 @@ def test_weights_have_no_bias(ctx, bits, tokens, heads, kv_heads):
     cache.v_scales.fill_(float(value))
     got = call(ctx, c).float()
     assert bool((got == 1 + 2.0 ** -7).all()), "%d of %d results on the lower side" % (int((got < 1.005).sum()), got.numel())
+
+
+def launched(ctx, names, f):
+    """f(), and how often each of the kernels ran in it."""
+    ctx.timing(",".join(names))
+    try:
+        got = f()
+        return got, [ctx.kernel_time(n)[1] for n in names]
+    finally:
+        ctx.timing(None)
+
+
+@pytest.mark.parametrize("bits,dim", [(8, 64), (4, 96), (8, 96), (4, 128), (8, 192), (4, 192), (8, 256)])
+def test_many_shares_are_joined(ctx, bits, dim):
+    """More than 16 shares of a row: several threads join each value, at head sizes that do and do not fill a workgroup."""
+    g = np.random.default_rng(40 + dim + bits)
+    c = attention_case(ctx, g, [4500], 2, 3, 1, dim, bits, 64, None)
+    got, (n,) = launched(ctx, ["k_attn_join"], lambda: call(ctx, c))
+    assert n == 1
+    check(got, c)
+    assert torch.equal(got, call(ctx, c))
