@@ -354,7 +354,8 @@ int gptq_gemm_wqa16(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, con
  * products; these operators have no counterpart there.)  All ASYNC on the
  * context's stream; device buffers, caller-owned.  They may be captured into
  * a HIP graph: the attention needs workspace, which its first call of a size
- * allocates, so run a call once before it is captured.  Element types of x, y, K
+ * allocates, so run a call once before it is captured (one that needs more
+ * while the stream is captured is refused: GPTQ_ERR_UNSUPPORTED).  Element types of x, y, K
  * and V: GPTQ_BF16 (bit patterns) or GPTQ_F32; their last dimension (the head)
  * is contiguous, the strides of tokens and heads are given in elements. */
 #define GPTQ_BF16 0

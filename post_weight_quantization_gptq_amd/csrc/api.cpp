@@ -165,12 +165,30 @@ int ensure(gptq_ctx c, DevBuf& b, size_t bytes) {
 
 // ensure() for buffers of calls that may be captured: an outgrown one is kept
 // until the context goes, since a graph captured with it may be replayed.  It
-// doubles, so that all of them take at most twice the last one.
-int ensure_kept(gptq_ctx c, DevBuf& b, size_t bytes) {
+// doubles, so that all of them take at most twice the last one.  Nothing is
+// allocated while the stream is being captured: that would end the capture, and
+// where it did not, `zero` would clear the buffer in the graph's replays only.
+// zero: a new buffer starts cleared; it is installed only once that is enqueued.
+int ensure_kept(gptq_ctx c, DevBuf& b, size_t bytes, bool zero = false) {
   if (b.cap >= bytes && b.p) return GPTQ_OK;
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(c->stream, &st) != hipSuccess) {  // the null stream, while another is being captured
+    (void)hipGetLastError();
+    st = hipStreamCaptureStatusActive;
+  }
+  if (st != hipStreamCaptureStatusNone)
+    return set_err(c, GPTQ_ERR_UNSUPPORTED,
+                   "the stream is being captured and the call needs more workspace: run it once before the capture");
   DevBuf next;
   const int rc = ensure(c, next, std::max(bytes, 2 * b.cap));
   if (rc) return rc;
+  if (zero) {
+    const hipError_t e = launch_zero_f32((float*)next.p, (long long)(next.cap / sizeof(float)), c->stream);
+    if (e != hipSuccess) {
+      (void)hipFree(next.p);
+      return set_err(c, GPTQ_ERR_HIP, "clearing %zu bytes: %s", next.cap, hipGetErrorString(e));
+    }
+  }
   if (b.p) c->outgrown.push_back(b.p);
   b = next;
   return GPTQ_OK;
@@ -1567,10 +1585,7 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
     p.info = (int*)(p.ml + 2 * rows);
   }
   if (fuse) {
-    const size_t had = c->counts.cap;
-    if ((rc = ensure_kept(c, c->counts, (size_t)seqs * cache->heads * p.nrb * sizeof(int)))) return rc;
-    if (c->counts.cap != had)
-      HIPCHK(c, launch_zero_f32((float*)c->counts.p, (long long)(c->counts.cap / sizeof(float)), c->stream));
+    if ((rc = ensure_kept(c, c->counts, (size_t)seqs * cache->heads * p.nrb * sizeof(int), true))) return rc;
     p.count = (int*)c->counts.p;
   }
   LAUNCH(c, p.wide ? "k_tree_attn_wide" : "k_tree_attn", launch_tree_attn(p, cache->bits, c->stream));

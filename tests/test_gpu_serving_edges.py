@@ -4,8 +4,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from post_weight_quantization_gptq_amd import Context  # noqa: E402
-from test_gpu_serving import attention_case, call, check  # noqa: E402
+from post_weight_quantization_gptq_amd import Context, GPTQError  # noqa: E402
+from test_gpu_serving import attention_case, call, check, i32  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,43 @@ def test_many_shares_are_joined(ctx, bits, dim):
     assert n == 1
     check(got, c)
     assert torch.equal(got, call(ctx, c))
+
+
+@pytest.mark.parametrize("mode", ["global", "thread_local", "relaxed"])
+def test_a_capture_takes_no_workspace(mode):
+    """A call that would have to grow its workspace is refused while its stream is captured; the capture goes on, and the
+    same call then runs eagerly and, its workspace there, in a graph."""
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        own = Context("cuda:0")
+        try:
+            g = np.random.default_rng(50)
+            c = attention_case(own, g, [700, 30], 1, 4, 2, 64, 8, 16, None)  # few shares: joined in the same launch
+            t, n = i32(c["tables"]), i32(c["lengths"])
+            out = torch.zeros_like(c["q"])
+            mark = torch.zeros(1, device="cuda:0")
+            side.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side, capture_error_mode=mode):
+                mark.add_(1)
+                with pytest.raises(GPTQError) as e:
+                    own.tree_attention(c["q"], c["cache"], t, n, out=out)
+            assert e.value.status == 4 and "capture" in str(e.value)
+            graph.replay()
+            side.synchronize()
+            assert float(mark) == 1 and not bool(out.any())
+            want = own.tree_attention(c["q"], c["cache"], t, n)
+            check(want, c)
+            again = torch.cuda.CUDAGraph()
+            side.synchronize()
+            with torch.cuda.graph(again, stream=side, capture_error_mode=mode):
+                own.tree_attention(c["q"], c["cache"], t, n, out=out)
+            for _ in range(3):
+                out.zero_()
+                again.replay()
+                side.synchronize()
+                assert torch.equal(out, want) and torch.equal(own.tree_attention(c["q"], c["cache"], t, n), want)
+            del graph, again
+        finally:
+            side.synchronize()
+            own.close()
