@@ -355,7 +355,11 @@ int gptq_gemm_wqa16(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, con
  * context's stream; device buffers, caller-owned.  They may be captured into
  * a HIP graph: the attention needs workspace, which its first call of a size
  * allocates, so run a call once before it is captured (one that needs more
- * while the stream is captured is refused: GPTQ_ERR_UNSUPPORTED).  Element types of x, y, K
+ * while the stream is captured is refused: GPTQ_ERR_UNSUPPORTED).  That workspace
+ * is the context's, also in a graph's replays: calls of a context and replays
+ * of graphs captured with it run one after the other, on one stream or ordered by
+ * events.  What overlaps (another stream, a graph beside eager calls) needs a context
+ * of its own, or results are wrong, later ones included.  Element types of x, y, K
  * and V: GPTQ_BF16 (bit patterns) or GPTQ_F32; their last dimension (the head)
  * is contiguous, the strides of tokens and heads are given in elements. */
 #define GPTQ_BF16 0

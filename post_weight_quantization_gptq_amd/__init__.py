@@ -217,7 +217,11 @@ class KVCache:
 
 
 class Context:
-    """A library context bound to a device and to the current torch stream."""
+    """A library context bound to a device and to the current torch stream.
+
+    Its workspace is shared by its calls and by replays of graphs captured with it: they must run one after the
+    other, on that stream or ordered by events.  For work that overlaps (another stream, a graph replayed beside eager
+    calls) make another Context."""
 
     def __init__(self, device=None):
         import torch
