@@ -449,7 +449,9 @@ int gptq_kv_read(gptq_ctx ctx, const gptq_kv_cache* cache, const int32_t* slots,
  * that sees nothing is zero, as is every row of a sequence with lengths < 0.
  * Query head hq reads cache head hq / (heads / cache.heads).  Q and O bf16
  * bits; scores, softmax and sums in fp32 (see the kernel for its operands).
- * Rows of Q 16-byte aligned, rows of O 8-byte aligned; width * page <= 2^29. */
+ * Rows of Q 16-byte aligned, rows of O 8-byte aligned; width * page <= 2^29; at
+ * most 2^26 rows (token, head) of a sequence and 2^23 .. 2^24 workgroups in all
+ * (GPTQ_ERR_UNSUPPORTED). */
 int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t* Q, int32_t seqs, int32_t tokens,
                         int32_t heads, int64_t q_seq, int64_t q_token, int64_t q_head, const int32_t* tables,
                         int32_t width, const int32_t* lengths, const uint32_t* mask, int32_t words, float scale,

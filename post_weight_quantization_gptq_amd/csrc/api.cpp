@@ -1473,8 +1473,7 @@ GPTQ_API int gptq_kv_write(gptq_ctx c, const gptq_kv_cache* cache, const void* K
   if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
   if (tokens == 0) return GPTQ_OK;
   if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if (tokens > INT32_MAX || (tokens + 63) / 64 * cache->heads > (1 << 28))
-    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens");
   if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
   if (cache->heads == 1) k_head = v_head = 0;
   if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))
@@ -1504,8 +1503,7 @@ GPTQ_API int gptq_kv_read(gptq_ctx c, const gptq_kv_cache* cache, const int32_t*
   if (bad_type(type)) return set_err(c, GPTQ_ERR_INVALID_ARG, "unknown element type");
   if (tokens == 0) return GPTQ_OK;
   if (!K || !V || !slots) return set_err(c, GPTQ_ERR_INVALID_ARG, "null buffer");
-  if (tokens > INT32_MAX || (tokens + 63) / 64 * cache->heads > (1 << 28))
-    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (tokens > INT32_MAX) return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many tokens");
   if (tokens == 1) k_token = v_token = 0;  // the stride of a dimension of one is never used
   if (cache->heads == 1) k_head = v_head = 0;
   if (!rows_of_4(K, type, k_token, k_head) || !rows_of_4(V, type, v_token, v_head))
@@ -1572,6 +1570,8 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   p.scale = scale * 1.4426950408889634f;
   DeviceGuard g(c->device);
   plan_tree_attn(p, c->ncu);
+  if (!attention_fits(p, (int64_t)seqs * cache->heads * tokens * p.group, cache->dim))
+    return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many rows for one launch");
   // Few shares of few rows are joined by the last workgroup of a row block: it
   // saves the second launch (1000 positions, 8 heads of 4 rows: 14.3 against
   // 17.3 us a call).  Where that workgroup would join many rows alone, a launch

@@ -1071,25 +1071,26 @@ namespace {
 template <int DIM, int BITS>
 void attn_nb(const AttnProb& p, dim3 grid, hipStream_t st) {
   constexpr int TP = DIM <= 128 ? 64 : 32;
+  const dim3 block(attention_threads(p, DIM));
   if (p.wide) {
     if (p.nb == 1)
-      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 1, TP>), grid, dim3(256), 0, st, p);
+      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 1, TP>), grid, block, 0, st, p);
     else if constexpr (DIM <= 128)
-      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 2, TP>), grid, dim3(256), 0, st, p);
+      hipLaunchKernelGGL((k_tree_attn_wide<DIM, BITS, 2, TP>), grid, block, 0, st, p);
   } else if (p.nb == 1) {
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, TP, 4, 2>), grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 1, TP, 4, 2>), grid, block, 0, st, p);
   } else if (p.nb == 2) {
     if constexpr (DIM <= 128)
-      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 8, 2>), grid, dim3(512), 0, st, p);
+      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 8, 2>), grid, block, 0, st, p);
     else
-      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 4, 1>), grid, dim3(256), 0, st, p);
+      hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 2, 32, 4, 1>), grid, block, 0, st, p);
   } else if constexpr (DIM <= 128) {
-    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 3, 32, 8, 2>), grid, dim3(512), 0, st, p);
+    hipLaunchKernelGGL((k_tree_attn<DIM, BITS, 3, 32, 8, 2>), grid, block, 0, st, p);
   }
 }
 template <int BITS>
 hipError_t attn_dim(const AttnProb& p, hipStream_t st) {
-  const dim3 grid((unsigned)((p.units + 7) / 8 * 8 * p.nrb));
+  const dim3 grid((unsigned)attention_blocks(p));
   switch (p.c.dim) {
     case 64: attn_nb<64, BITS>(p, grid, st); break;
     case 96: attn_nb<96, BITS>(p, grid, st); break;

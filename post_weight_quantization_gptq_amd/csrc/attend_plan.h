@@ -69,3 +69,14 @@ struct JoinThread {
 constexpr JoinThread join_thread(int tid, int dim, int G) {
   return JoinThread{tid / (dim / 4 * G), tid / (dim / 4) % G, 4 * (tid % (dim / 4))};
 }
+
+// Workgroups of the attention's launch (rounded up for the XCDs) and their threads.
+inline long long attention_blocks(const AttnPlan& p) { return ((long long)p.units + 7) / 8 * 8 * p.nrb; }
+inline int attention_threads(const AttnPlan& p, int dim) { return !p.wide && p.nb > 1 && dim <= 128 ? 512 : 256; }
+// Whether the threads of both launches can be counted in 32 bits (rows: of all
+// sequences and query heads).
+inline bool attention_fits(const AttnPlan& p, long long rows, int dim) {
+  const JoinPlan j = plan_join(dim, p.shares);
+  const long long join = p.most > 1 ? (rows + j.rows - 1) / j.rows * j.threads : 0;
+  return attention_blocks(p) * attention_threads(p, dim) < 1LL << 32 && join < 1LL << 32;
+}

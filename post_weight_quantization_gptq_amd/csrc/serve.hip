@@ -71,17 +71,17 @@ __device__ __forceinline__ void store_vals(float* p, const float* v) {
 }  // namespace
 
 // ---------------------------------------------------------------- rotary --
-// table[p][0][i] = mag cos(p f_i), table[p][1][i] = mag sin(p f_i): the angle
-// and its cosine in fp64 (p f_i passes 1e5, where an fp32 angle would be off
-// by 1e-2), rounded once.  Made once for a model; not tuned.
-__global__ __launch_bounds__(256) void k_rope_table(const RopeFreq f, int length, int half, double mag,
+// table[p][0][i] = mag cos(p f_i), table[p][1][i] = mag sin(p f_i), rows from
+// position `first` on: the angle and its cosine in fp64 (p f_i passes 1e5, where an
+// fp32 angle would be off by 1e-2), rounded once.  Made once for a model; not tuned.
+__global__ __launch_bounds__(256) void k_rope_table(const RopeFreq f, int first, int length, int half, double mag,
                                                     float* __restrict__ table) {
   const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
   if (idx >= (long long)length * half) return;
   const long long p = idx / half;
   const int i = (int)(idx % half);
   double s, c;
-  sincos((double)p * f.f[i], &s, &c);
+  sincos((double)(first + p) * f.f[i], &s, &c);
   table[p * 2 * half + i] = (float)(mag * c);
   table[p * 2 * half + half + i] = (float)(mag * s);
 }
@@ -405,8 +405,12 @@ __global__ __launch_bounds__(256) void k_kv_read(const KvReadProb p) {
 
 // ------------------------------------------------------------- launchers --
 hipError_t launch_rope_table(const RopeFreq& f, int length, int half, double mag, float* table, hipStream_t st) {
-  const long long n = (long long)length * half;
-  hipLaunchKernelGGL(k_rope_table, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, f, length, half, mag, table);
+  const long long most = (1LL << 31) / half;  // positions a launch: its threads are counted in 32 bits
+  for (long long t = 0; t < length; t += most) {
+    const int n = (int)std::min(most, length - t);
+    const dim3 grid((unsigned)(((long long)n * half + 255) / 256));
+    hipLaunchKernelGGL(k_rope_table, grid, dim3(256), 0, st, f, (int)t, n, half, mag, table + t * 2 * half);
+  }
   return hipGetLastError();
 }
 
@@ -454,12 +458,21 @@ hipError_t rope_l(const RopeProb& p, int layout, hipStream_t st) {
   return layout ? rope_v<TX, TY, true>(p, st) : rope_v<TX, TY, false>(p, st);
 }
 
-// 64 tokens a workgroup where that makes 512 of them, else 16
+// 64 tokens a workgroup where that makes 512 of them, else 16; as many tokens a
+// launch as keep its threads under 2^32
 template <class T, int BITS, int D, class P>
 void kv_launch(const P& p, hipStream_t st, void (*wide)(P), void (*narrow)(P)) {
   const bool w = (p.tokens + 63) / 64 * p.c.heads >= 256;
-  const dim3 grid((unsigned)(((p.tokens + (w ? 63 : 15)) / (w ? 64 : 16) + 7) / 8 * 8 * p.c.heads * 2));
-  hipLaunchKernelGGL(w ? wide : narrow, grid, dim3(256), 0, st, p);
+  const long long tw = w ? 64 : 16, most = ((1LL << 24) - 1) / (2 * p.c.heads) / 8 * 8 * tw;
+  for (long long t = 0; t < p.tokens; t += most) {
+    P q = p;
+    q.tokens = std::min(most, p.tokens - t);
+    q.k = (decltype(q.k))((uintptr_t)p.k + t * p.kt * sizeof(T));
+    q.v = (decltype(q.v))((uintptr_t)p.v + t * p.vt * sizeof(T));
+    q.slots = p.slots + t;
+    const dim3 grid((unsigned)(((q.tokens + tw - 1) / tw + 7) / 8 * 8 * p.c.heads * 2));
+    hipLaunchKernelGGL(w ? wide : narrow, grid, dim3(256), 0, st, q);
+  }
 }
 template <class T, int BITS, int D>
 void kv_one(const KvWriteProb& p, hipStream_t st) {

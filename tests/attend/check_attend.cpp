@@ -40,7 +40,31 @@ static void check_join(int dim, int shares) {
   for (size_t i = 0; i < hit.size(); ++i) CHECK(hit[i] == 1, "dim %d: part %zu has %d threads", dim, i, hit[i]);
 }
 
+// A plan that is said to fit: no number of it has overflowed, and the launches' threads are fewer than 2^32; one
+// that is said not to: they are not.
+static void check_limits(long long R, int seqs, int kv_heads, int dim, long long hold) {
+  const AttnPlan p = plan_attention(R, seqs, kv_heads, dim, hold, 256);
+  const __int128 rows = (__int128)R * seqs * kv_heads;
+  const int block = p.wide ? (p.nb == 1 ? 64 : 128) : 16 * p.nb;
+  CHECK((long long)p.nrb * block >= R && (long long)(p.nrb - 1) * block < R, "R %lld: %d blocks of %d", R, p.nrb, block);
+  CHECK(p.nb >= 1 && p.nb <= (p.wide ? (dim <= 128 ? 2 : 1) : dim <= 128 ? 3 : 2), "R %lld dim %d: nb %d", R, dim, p.nb);
+  CHECK(p.units >= (long long)seqs * kv_heads && p.kept >= 0 && p.fit >= 1, "seqs %d heads %d: %d units", seqs, kv_heads, p.units);
+  const JoinPlan j = plan_join(dim, p.shares);
+  // k_tree_attn: four waves for up to 16 rows and for heads above 128, else eight; k_tree_attn_wide: four
+  const int waves = p.wide || p.nb == 1 || dim > 128 ? 4 : 8;
+  const __int128 attn = ((__int128)p.units + 7) / 8 * 8 * p.nrb * waves * 64;
+  const __int128 join = p.most > 1 ? (rows + j.rows - 1) / j.rows * j.threads : 0;
+  const bool small = attn < (__int128)1 << 32 && join < (__int128)1 << 32;
+  CHECK(attention_fits(p, (long long)rows, dim) == small, "R %lld seqs %d heads %d dim %d", R, seqs, kv_heads, dim);
+}
+
 int main() {
+  for (int dim : {64, 96, 128, 192, 256})
+    for (long long R : {1LL, 16LL, 17LL, 48LL, 49LL, 64LL, 65LL, 128LL, 129LL, 1000LL, 1LL << 20, 1LL << 26})
+      for (int heads : {1, 3, 8, 64, 65535})
+        for (int seqs : {1, 2, 65, 4096, 1 << 18, 1 << 20, 1 << 24, 1 << 28})
+          for (long long hold : {0LL, 1LL, 64LL, 1LL << 21})
+            if ((__int128)R * heads <= 1 << 26 && (__int128)R * heads * seqs <= 1 << 30) check_limits(R, seqs, heads, dim, hold);
   for (int dim : {64, 96, 128, 192, 256})
     for (int shares : {2, 3, 8, 9, 15, 16, 17, 64, 512}) check_join(dim, shares);
   if (g_fail) return 1;

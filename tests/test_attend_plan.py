@@ -43,6 +43,8 @@ def test_shapes_pass_the_checker(tmp_path):
 MISTAKES = [
     ("join-threads-past-the-rows", "return JoinPlan{G, rows, rows * q4 * G};", "return JoinPlan{G, rows, 256};", "reads sum"),
     ("join-partners-a-row-apart", "tid / (dim / 4) % G, 4 * (tid % (dim / 4))", "tid % G, 4 * (tid / G % (dim / 4))", "partner"),
+    ("threads-of-a-launch-in-33-bits", "attention_threads(p, dim) < 1LL << 32 &&", "attention_threads(p, dim) < 1LL << 33 &&", "seqs"),
+    ("rows-of-a-join-not-counted", "join < 1LL << 32", "join >= 0", "seqs"),
 ]
 
 

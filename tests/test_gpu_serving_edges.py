@@ -4,8 +4,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from post_weight_quantization_gptq_amd import Context, GPTQError  # noqa: E402
-from test_gpu_serving import attention_case, call, check, i32  # noqa: E402
+from oracle import serving_ref as o  # noqa: E402
+from post_weight_quantization_gptq_amd import Context, GPTQError, KVCache  # noqa: E402
+from test_gpu_serving import attention_case, call, check, fill, i32, up  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,69 @@ def test_a_capture_takes_no_workspace(mode):
         finally:
             side.synchronize()
             own.close()
+
+
+# ---------------------------------------------------- more than one launch --
+MANY = (1 << 23) + 100  # tokens of 64 heads: more workgroups of 256 than 2^32 threads make
+
+
+def test_write_of_more_tokens_than_a_launch_holds(ctx):
+    """All tokens are skipped but a few: the first, the last, and those round the end of what one launch can hold."""
+    heads, dim, tokens = 64, 64, MANY
+    at = [0, 1, 8388000, 8388095, 8388096, 8388097, tokens - 2, tokens - 1]
+    x = torch.zeros((tokens, 1, dim), dtype=torch.bfloat16, device="cuda:0")
+    x[at] = torch.randn((len(at), 1, dim), generator=torch.Generator().manual_seed(60)).to(torch.bfloat16).cuda()
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device="cuda:0")
+    slots[at] = i32(range(3, 3 + len(at)))
+    few = x[at].expand(-1, heads, -1).contiguous()
+    got, want = (ctx.kv_cache(2, heads, dim, 8, 16) for _ in range(2))
+    fill(got)
+    fill(want)
+    ctx.kv_write(got, x.expand(-1, heads, -1), x.flip(2).expand(-1, heads, -1), slots)
+    ctx.kv_write(want, few, few.flip(2), i32(range(3, 3 + len(at))))
+    for n in KVCache.FIELDS:
+        assert torch.equal(getattr(got, n).nan_to_num(7.0), getattr(want, n).nan_to_num(7.0)), n
+
+
+def test_read_of_more_tokens_than_a_launch_holds(ctx):
+    """Heads that hold the same, read into one place: every head writes the same values."""
+    heads, dim, tokens = 64, 64, MANY
+    cache, one = ctx.kv_cache(4, heads, dim, 8, 16), ctx.kv_cache(4, 1, dim, 8, 16)
+    rows = torch.randn((64, 2, dim), generator=torch.Generator().manual_seed(61)).cuda()
+    where = torch.arange(64, dtype=torch.int32, device="cuda:0")
+    ctx.kv_write(cache, rows[:, :1].expand(-1, heads, -1), rows[:, 1:].expand(-1, heads, -1), where)
+    ctx.kv_write(one, rows[:, :1], rows[:, 1:], where)
+    slots = torch.randint(-1, 64, (tokens,), generator=torch.Generator().manual_seed(62)).to(torch.int32).cuda()
+    k, v = (torch.full((tokens, 1, dim), 9.0, dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+    ctx.kv_read(cache, slots, k=k.expand(-1, heads, -1), v=v.expand(-1, heads, -1))
+    for a, b in zip((k, v), ctx.kv_read(one, slots)):
+        assert torch.equal(a, b)
+
+
+def test_rope_table_of_more_values_than_a_launch_holds(ctx):
+    """2^32 pairs and some: two launches."""
+    length, rot = (1 << 25) + 3, 256
+    table = ctx.rope_table(length, rot)
+    short = ctx.rope_table(5, rot)
+    assert torch.equal(table[:5], short)
+    w = o.rope_frequencies(rot)
+    for p in ((1 << 24) - 1, 1 << 24, (1 << 24) + 1, (1 << 25) - 1, 1 << 25, length - 1):
+        row = up(table[p])  # an angle of 2^25 in float64 is within 2^-28 of its own
+        assert np.abs(row[0] - np.cos(p * w)).max() <= 2.0 ** -24 + 1e-8
+        assert np.abs(row[1] - np.sin(p * w)).max() <= 2.0 ** -24 + 1e-8
+
+
+def test_attention_of_more_rows_than_a_launch_holds(ctx):
+    """2^24 workgroups are refused before anything is launched."""
+    seqs, heads = 1 << 20, 16
+    cache = ctx.kv_cache(1, heads, 64, 8, 16)
+    q = torch.zeros((1, 1, heads, 64), dtype=torch.bfloat16, device="cuda:0").expand(seqs, -1, -1, -1)
+    t, n = torch.zeros((seqs, 1), dtype=torch.int32, device="cuda:0"), torch.zeros(seqs, dtype=torch.int32, device="cuda:0")
+
+    def refused():
+        with pytest.raises(GPTQError) as e:
+            ctx.tree_attention(q, cache, t, n, out=torch.empty_like(q))
+        return e.value
+
+    err, launches = launched(ctx, ["k_tree_attn", "k_tree_attn_wide", "k_attn_join"], refused)
+    assert err.status == 4 and "rows" in str(err) and launches == [0, 0, 0]
