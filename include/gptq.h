@@ -449,6 +449,8 @@ int gptq_kv_read(gptq_ctx ctx, const gptq_kv_cache* cache, const int32_t* slots,
  * that sees nothing is zero, as is every row of a sequence with lengths < 0.
  * Query head hq reads cache head hq / (heads / cache.heads).  Q and O bf16
  * bits; scores, softmax and sums in fp32 (see the kernel for its operands).
+ * Any finite queries and scale; keys and values of at most 2^100 in magnitude (the
+ * sums of larger ones may pass fp32's range), zero points at most 2^bits - 1.
  * Rows of Q 16-byte aligned, rows of O 8-byte aligned; width * page <= 2^29; at
  * most 2^26 rows (token, head) of a sequence and 2^23 .. 2^24 workgroups in all
  * (GPTQ_ERR_UNSUPPORTED). */

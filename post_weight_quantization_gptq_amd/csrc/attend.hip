@@ -279,7 +279,11 @@ __device__ __forceinline__ float query_row(const AttnProb& p, int b, int h, int 
   }
   mx = max_groups(mx);
   const int ex = (int)(__float_as_uint(mx) >> 23);
-  const int up = ex == 0 || ex == 255 ? 0 : min(141 - ex, 100);  // 2^up mx in [2^14, 2^15)
+  // 2^up mx in [2^14, 2^15), or less where the factor would fall under 2^-118: a
+  // position that is not seen has the score NONE, and NONE times the factor (-2^10)
+  // has to lie far below every other score
+  const int es = (int)(__float_as_uint(fabsf(p.scale)) >> 23) - 127;
+  const int up = ex == 0 || ex == 255 ? 0 : min(141 - ex, min(100, 118 + es));
   float f = __uint_as_float((uint32_t)(127 + up) << 23);
   if (p.scale < 0.f) f = -f;
   if (p.scale == 0.f) f = 0.f;
@@ -292,8 +296,8 @@ __device__ __forceinline__ float query_row(const AttnProb& p, int b, int h, int 
       out[ks][j] = pack16(v[ks][2 * j] * fj, v[ks][2 * j + 1] * fj);
     }
   }
-  // (a factor under 2^-100 leaves every weight at 1, as 2^-100 does)
-  return fmaxf(fabsf(p.scale) * __uint_as_float((uint32_t)(127 - up) << 23), 0x1p-100f);
+  // (less only for a scale of 0, or for one under 2^-118 with queries under 2^-126)
+  return fmaxf(fabsf(p.scale) * __uint_as_float((uint32_t)(127 - up) << 23), 0x1p-118f);
 }
 
 // Eight key codes as an operand, less their zero point: zl = 1024 + z twice, zh

@@ -163,3 +163,17 @@ def test_attention_of_more_rows_than_a_launch_holds(ctx):
 
     err, launches = launched(ctx, ["k_tree_attn", "k_tree_attn_wide", "k_attn_join"], refused)
     assert err.status == 4 and "rows" in str(err) and launches == [0, 0, 0]
+
+
+# ------------------------------------------------------------ score factors --
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens,heads", [(1, 4), (20, 1), (70, 2)])
+@pytest.mark.parametrize("queries,keys,scale", [(1e-28, 1e28, None), (1e-33, 1e33, None), (1.0, 1e29, 1e-30),
+                                                (1e-5, 1e34, 1e-30), (1e30, 1e-30, None), (1e25, 1e-5, 1e-21)])
+def test_factors_far_from_one(ctx, bits, tokens, heads, queries, keys, scale):
+    """Queries, keys and a scale far from one whose scores are ordinary."""
+    g = np.random.default_rng(70 + bits + tokens)
+    c = attention_case(ctx, g, [80, 33], tokens, heads, 1, 64, bits, 16, None)
+    c["q"] = (c["q"].float() * queries).to(torch.bfloat16)
+    c["cache"].k_scales.mul_(keys)
+    check(call(ctx, c, scale=scale), c, scale=scale)
