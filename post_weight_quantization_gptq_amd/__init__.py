@@ -187,7 +187,9 @@ class KVCache:
 
     ``k_codes`` uint8 [pages, heads, page, dim*bits/8], ``v_codes`` uint8
     [pages, heads, dim*bits/8, page], ``k_scales``/``v_scales`` float32 and
-    ``k_zeros``/``v_zeros`` uint8 [pages, heads, page]."""
+    ``k_zeros``/``v_zeros`` uint8 [pages, heads, page].  The tensors are filled
+    in place; another tensor in the place of one takes a new KVCache, and
+    setting an attribute to one raises AttributeError."""
 
     FIELDS = ("k_codes", "k_scales", "k_zeros", "v_codes", "v_scales", "v_zeros")
 
@@ -214,6 +216,12 @@ class KVCache:
         self.device = k_codes.device
         self._index = self.device.index
         self._c = _KV(*[t.data_ptr() for t in given], pages, heads, page, self.dim, bits, 0)
+
+    def __setattr__(self, name, value):
+        # calls pass the pointers of the tensors that were checked (`x *= 2` sets the same tensor again)
+        if "_c" in self.__dict__ and getattr(self, name, None) is not value:
+            raise AttributeError("a KVCache is fixed: make another for other tensors (%s)" % name)
+        object.__setattr__(self, name, value)
 
 
 class Context:

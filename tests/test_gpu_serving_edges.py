@@ -177,3 +177,21 @@ def test_factors_far_from_one(ctx, bits, tokens, heads, queries, keys, scale):
     c["q"] = (c["q"].float() * queries).to(torch.bfloat16)
     c["cache"].k_scales.mul_(keys)
     check(call(ctx, c, scale=scale), c, scale=scale)
+
+
+# ------------------------------------------------------------------- handle --
+def test_a_cache_keeps_its_tensors(ctx):
+    """Other tensors in the place of a cache's are refused, not ignored; the same ones change in place."""
+    cache = ctx.kv_cache(2, 1, 64, 8, 16)
+    x = torch.randn((3, 1, 64), generator=torch.Generator().manual_seed(80)).cuda()
+    ctx.kv_write(cache, x, x, i32([0, 5, 31]))
+    k, v = ctx.kv_read(cache, i32([0, 5, 31]), dtype=torch.float32)
+    for name in KVCache.FIELDS:
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name).clone())
+    for name, value in (("bits", 4), ("page", 32), ("pages", 9)):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, value)
+    cache.v_scales *= 2.0
+    k2, v2 = ctx.kv_read(cache, i32([0, 5, 31]), dtype=torch.float32)
+    assert torch.equal(k2, k) and torch.equal(v2, 2 * v)
