@@ -159,8 +159,8 @@ def visible(lengths, tokens, mask, b, t, capacity):
 
 def tree_attention(q, pool, tables, lengths, bits, mask=None, scale=None):
     """(o, spread, top) in float64: o [seqs, tokens, heads, dim]; for error bounds, spread = sum_j p_j |v_j| of
-    every output and top [seqs, tokens, heads] = the largest |scale q| . s_k sum |q| factor of a row's scores
-    and the largest |score|."""
+    every output and top [seqs, tokens, heads, 2] = the largest scale sum_d |q_d| |k_jd| of a row's scores and the
+    largest |score|."""
     q = np.asarray(q, np.float64)
     seqs, tokens, heads, dim = q.shape
     pages, kv_heads, page, _ = pool["k_codes"].shape
@@ -176,18 +176,17 @@ def tree_attention(q, pool, tables, lengths, bits, mask=None, scale=None):
             if not pos:
                 continue
             for h in range(kv_heads):
-                ks, vs, sk = [], [], []
+                ks, vs = [], []
                 for j in pos:
                     key = (int(tables[b, j // page]), h, j % page)
                     if key not in rows:
                         kq, vq = kv_codes(pool, *key, bits)
                         s, z = float(pool["k_scales"][key]), float(pool["k_zeros"][key])
                         sv, zv = float(pool["v_scales"][key]), float(pool["v_zeros"][key])
-                        rows[key] = (s * (kq.astype(np.float64) - z), sv * (vq.astype(np.float64) - zv), abs(s))
-                    kr, vr, s = rows[key]
+                        rows[key] = s * (kq.astype(np.float64) - z), sv * (vq.astype(np.float64) - zv)
+                    kr, vr = rows[key]
                     ks.append(kr)
                     vs.append(vr)
-                    sk.append(s)
                 ks, vs = np.array(ks), np.array(vs)
                 for g in range(group):
                     row = q[b, t, h * group + g]
@@ -196,14 +195,26 @@ def tree_attention(q, pool, tables, lengths, bits, mask=None, scale=None):
                     p /= p.sum()
                     o[b, t, h * group + g] = p @ vs
                     spread[b, t, h * group + g] = p @ np.abs(vs)
-                    top[b, t, h * group + g] = abs(scale) * max(sk) * np.abs(row).sum(), np.abs(x).max()
+                    top[b, t, h * group + g] = abs(scale) * (np.abs(ks) @ np.abs(row)).max(), np.abs(x).max()
     return o, spread, top
 
 
+def bf16(x):
+    """float64 rounded to 8 significant bits, ties to even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256.0), e - 8)
+
+
 def attention_bound(o, spread, top, dim):
-    """Largest allowed |error| of a bf16 result.  Scores are sums of dim products of magnitude up to 1279 s_k |q|
-    in float32 (codes enter as 1024 + code), random-walk growth with a factor of four; the exponent's argument is
-    itself rounded (2^-22 of the largest score); weights times scales are held in 11 bits; the result is rounded to
-    8 bits."""
-    delta = 4.0 * math.sqrt(dim) * 2.0 ** -24 * 1279.0 * top[..., 0] + 2.0 ** -21 * top[..., 1]
-    return 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2.0 * delta[..., None]) * spread + 1e-30
+    """Largest allowed |error| of a bf16 result, from the widths of the operands.
+
+    Scores: queries (bf16, times a power of two) and code - zero point are exact in float16 and so are their products
+    in float32; their sum over dim has float32's roundings, random-walk growth with a factor of four.  Its products
+    with the scale and the factor to powers of two, the reference and their difference: 2^-21 of the largest score.
+    Weights: times their position's scale, two bfloat16 numbers to nearest, 2^-16.  Sums over up to 2^14
+    positions in float32, random-walk growth with a factor of four: 2^-15.  All of that is relative to spread,
+    with the scores' error twice (weight and sum).  The result is then rounded to bf16: it lies between the rounded
+    ends of that interval, which for most values are the same number."""
+    delta = 4.0 * math.sqrt(dim) * 2.0 ** -24 * top[..., 0] + 2.0 ** -21 * top[..., 1]
+    eps = (2.0 ** -16 + 2.0 ** -15 + 2.0 * delta[..., None]) * spread
+    return np.maximum(np.abs(bf16(o + eps) - o), np.abs(bf16(o - eps) - o)) + 1e-30
