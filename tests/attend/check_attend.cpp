@@ -58,7 +58,27 @@ static void check_limits(long long R, int seqs, int kv_heads, int dim, long long
   CHECK(attention_fits(p, (long long)rows, dim) == small, "R %lld seqs %d heads %d dim %d", R, seqs, kv_heads, dim);
 }
 
+// The kernel that takes a call of R rows a key head: the GPU tests take these row counts to reach every one.
+static void check_choice(int dim, long long R, int wide, int nb, int nrb) {
+  const AttnPlan p = plan_attention(R, 1, 1, dim, 2, 256);
+  CHECK(!!p.wide == !!wide && p.nb == nb && p.nrb == nrb, "dim %d rows %lld: wide %d, nb %d, %d blocks", dim, R, p.wide, p.nb, p.nrb);
+}
+
 int main() {
+  for (int dim : {64, 96, 128}) {
+    check_choice(dim, 10, 0, 1, 1);
+    check_choice(dim, 20, 0, 2, 1);
+    check_choice(dim, 40, 0, 3, 1);
+    check_choice(dim, 64, 1, 1, 1);
+    check_choice(dim, 80, 0, 3, 2);
+    check_choice(dim, 128, 1, 2, 1);
+  }
+  for (int dim : {192, 256}) {
+    check_choice(dim, 10, 0, 1, 1);
+    check_choice(dim, 20, 0, 2, 1);
+    check_choice(dim, 64, 1, 1, 1);
+    check_choice(dim, 80, 0, 2, 3);
+  }
   for (int dim : {64, 96, 128, 192, 256})
     for (long long R : {1LL, 16LL, 17LL, 48LL, 49LL, 64LL, 65LL, 128LL, 129LL, 1000LL, 1LL << 20, 1LL << 26})
       for (int heads : {1, 3, 8, 64, 65535})

@@ -195,3 +195,44 @@ def test_a_cache_keeps_its_tensors(ctx):
     cache.v_scales *= 2.0
     k2, v2 = ctx.kv_read(cache, i32([0, 5, 31]), dtype=torch.float32)
     assert torch.equal(k2, k) and torch.equal(v2, 2 * v)
+
+
+# ------------------------------------------------------------ every kernel --
+def wide(dim, rows):
+    """Whether k_tree_attn_wide takes these rows of a key head (tests/attend/check_attend.cpp holds the same table)."""
+    return rows == 64 or rows == 128 and dim <= 128
+
+
+BRANCHES = [(dim, rows) for dim in (64, 96, 128, 192, 256) for rows in ((10, 20, 40, 64, 80, 128) if dim <= 128 else (10, 20, 64, 80))]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dim,rows", BRANCHES)
+def test_every_attention_kernel(ctx, bits, dim, rows):
+    """Each (head size, width, rows a wave, kernel) there is: ragged trees on small pages, and a chain whose context is cut
+    into shares, joined by a launch of its own."""
+    g = np.random.default_rng(90 + dim + rows + bits)
+    names = ["k_tree_attn", "k_tree_attn_wide", "k_attn_join"]
+    one = [0, 1] if wide(dim, rows) else [1, 0]
+    c = attention_case(ctx, g, [330, 0, 61], rows // 2, 4, 2, dim, bits, 16, "tree")
+    got, n = launched(ctx, names, lambda: call(ctx, c))
+    assert n[:2] == one
+    check(got, c)
+    c = attention_case(ctx, g, [4200], rows // 2, 2, 1, dim, bits, 64, None)
+    got, n = launched(ctx, names, lambda: call(ctx, c))
+    assert n == one + [1]
+    check(got, c)
+    assert torch.equal(got, call(ctx, c))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_shares_joined_in_the_same_launch(ctx, bits, dim):
+    """Up to eight shares of up to 16 rows: the workgroup that comes last joins them, call after call."""
+    g = np.random.default_rng(95 + dim + bits)
+    c = attention_case(ctx, g, [1900, 700, 0], 2, 6, 2, dim, bits, 32, None)
+    got, n = launched(ctx, ["k_tree_attn", "k_attn_join"], lambda: call(ctx, c))
+    assert n == [1, 0]
+    check(got, c)
+    for _ in range(20):
+        assert torch.equal(got, call(ctx, c))
