@@ -154,9 +154,12 @@ __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
 // step in fp32: lo = min(v, 0), hi = max(v, 0), s = (hi - lo) fl32(1 / maxq),
 // r = 1 / s, z = rne(-lo r).  A range under 2^-100 (r would overflow) is
 // stored as zeros on s = 1; a row with a NaN or an infinity, or whose range
-// overflows, gets s = NaN and so reads back as NaN.  (s by a product: where -lo /
-// s lies half way between two zero points its last bit decides, and elementwise
-// tensor code divides by a constant so.)
+// overflows, gets s = NaN and so reads back as NaN.  The step is the product by
+// definition.  The correctly rounded quotient (hi - lo) / maxq, which the weights'
+// grids take, is up to one rounding apart; where -lo / s lies half way between two
+// zero points (rows with hi = -lo, common in bf16) it may give the other one.  A
+// product is what elementwise tensor code on this GPU makes of a division by a
+// constant, so that a cache filled by such code holds the same codes.
 struct KvGrid {
   float s, r, z;
 };

@@ -7,6 +7,7 @@ torch = pytest.importorskip("torch")
 from oracle import serving_ref as o  # noqa: E402
 from post_weight_quantization_gptq_amd import Context, GPTQError, KVCache  # noqa: E402
 from test_gpu_serving import attention_case, call, check, fill, i32, up  # noqa: E402
+from test_oracle_serving_grid import PINS  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +237,20 @@ def test_shares_joined_in_the_same_launch(ctx, bits, dim):
     check(got, c)
     for _ in range(20):
         assert torch.equal(got, call(ctx, c))
+
+
+# --------------------------------------------------------------------- grid --
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bits,a,zero,codes", PINS)
+def test_the_grid_s_step_is_a_product(ctx, dtype, bits, a, zero, codes):
+    """Rows on which the product and the quotient by maxq choose different zero points."""
+    x = torch.zeros((1, 1, 64), dtype=dtype, device="cuda:0")
+    x[0, 0, :3] = torch.tensor([a, -a, a / 2])
+    cache = ctx.kv_cache(1, 1, 64, bits, 16)
+    ctx.kv_write(cache, x, x, i32([9]))
+    s = np.float32(np.float32(2 * a) * np.float32(np.float32(1) / np.float32((1 << bits) - 1)))
+    for scales, zeros in ((cache.k_scales, cache.k_zeros), (cache.v_scales, cache.v_zeros)):
+        assert float(scales[0, 0, 9]) == float(s) and int(zeros[0, 0, 9]) == zero
+    want = np.float32(s) * (np.array(codes, np.float32) - np.float32(zero))
+    for r in ctx.kv_read(cache, i32([9]), dtype=torch.float32):
+        assert r[0, 0, :3].cpu().numpy().tolist() == want.tolist() and not bool(r[0, 0, 3:].any())
