@@ -5,10 +5,18 @@
 
 #include <algorithm>
 
-// Outputs from this size on are stored past the caches: they pass through the
-// eight 4 MB L2 before anyone reads them, and would push the inputs out of the
-// caches behind.  134 MB of values read back: 32 us, 71 with ordinary stores.
-#define STREAM_BYTES (32LL << 20)
+// Outputs from the last-level cache's size on are stored past the caches: what
+// reads them next would not find them there, and they push out what is.  Smaller
+// ones are left in the caches for it.  Past them, and ordinary, us:
+//   read back           64 MB   128 MB   192 MB   256 MB   384 MB
+//   alone               19, 19  33, 43   47, 63   79, 83   114, 119
+//   and copied          45, 40  91, 86   142, 150 182, 187 266, 268
+//   and its maximum     58, 54  94, 82   129, 109 162, 164 230, 238
+//   rotary              64 MB   128 MB   192 MB   256 MB   384 MB
+//   alone               34, 36  69, 71   102, 105 136, 138 201, 205
+//   and copied          62, 56  124, 126 183, 181 243, 240 357, 358
+//   and its maximum     62, 56  111, 101 161, 160 210, 211 310, 314
+#define STREAM_BYTES (256LL << 20)
 
 namespace {
 
@@ -90,7 +98,7 @@ __global__ __launch_bounds__(256) void k_rope_table(const RopeFreq f, int first,
 // (2i, 2i + 1) (interleaved) of the first rot values of every head; the other
 // values are copied.  A thread takes V pairs of one (token, head); a position
 // outside the table gives NaN.  Bound by HBM: 8192 tokens of 40 heads of 128
-// from float32 to bf16, 256 MB in 45 us, 5.6 TB/s; a few tokens by the launch, 3.4 us.
+// from float32 to bf16, 256 MB in 43 us, 5.9 TB/s; a few tokens by the launch, 3.3 us.
 template <class TX, class TY, int V, bool INTER, bool STREAM>
 __global__ __launch_bounds__(256) void k_rope(const RopeProb p) {
   const int half = p.rot / 2;
@@ -230,7 +238,7 @@ __device__ __forceinline__ long long kv_window(const KvPool& c, int& h, int& kv)
 // blocks of 4 tokens x 4 dimensions are transposed in registers, so that the
 // tokens of a dimension, which lie side by side in the pool, leave as words
 // where four slots follow each other inside a page.  Bound by HBM: 8194 tokens
-// of 8 heads of 128 from float32 to 4 bits, 76 MB in 17 us, 4.4 TB/s (22 us with
+// of 8 heads of 128 from float32 to 4 bits, 76 MB in 16 us, 4.6 TB/s (22 us with
 // one byte of a dimension at a time); 16 tokens 5 us.
 template <class T, int BITS, int D, int TW>
 __global__ __launch_bounds__(256) void k_kv_write(const KvWriteProb p) {
@@ -322,8 +330,7 @@ __global__ __launch_bounds__(256) void k_kv_write(const KvWriteProb p) {
 // ------------------------------------------------------------ cache read --
 // The inverse, laid out the same: fl32(s (q - z)), rounded once to the output
 // type; a slot outside the pool reads as zeros.  Bound by HBM: 32768 tokens of 8
-// heads of 128, 8 bits to bf16, 204 MB in 31 us, 6.5 TB/s with the results past
-// the caches; 300 tokens 3.7 us.
+// heads of 128, 8 bits to bf16, 204 MB in 41 us, 4.9 TB/s; 300 tokens 3.6 us.
 template <class T, int BITS, int D, int TW>
 __global__ __launch_bounds__(256) void k_kv_read(const KvReadProb p) {
   constexpr int RB = D * BITS / 8, PITCH = RB + 4, L = D / 8;
@@ -430,7 +437,7 @@ hipError_t rope_v(const RopeProb& p, hipStream_t st) {
            (uintptr_t)p.table % (4 * v) == 0;
   };
   // eight where the result is bf16, so that a store is 16 bytes (a prompt of
-  // 8192 x 40 heads of 128 from float32: 45 us, 53 with four)
+  // 8192 x 40 heads of 128 from float32: 43 to 45 us, 53 with four)
   const int v = sizeof(TY) == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
   const int nth = p.dim / (2 * v);
   const bool stream = p.tokens * p.heads * p.dim * (long long)sizeof(TY) >= STREAM_BYTES;

@@ -254,3 +254,34 @@ def test_the_grid_s_step_is_a_product(ctx, dtype, bits, a, zero, codes):
     want = np.float32(s) * (np.array(codes, np.float32) - np.float32(zero))
     for r in ctx.kv_read(cache, i32([9]), dtype=torch.float32):
         assert r[0, 0, :3].cpu().numpy().tolist() == want.tolist() and not bool(r[0, 0, 3:].any())
+
+
+# ---------------------------------------------------------- large results --
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("tin,tout,rot", [(torch.float32, torch.bfloat16, 64), (torch.bfloat16, torch.float32, 128),
+                                          (torch.float32, torch.float32, 40), (torch.bfloat16, torch.bfloat16, 128)])
+def test_rope_results_past_the_caches(ctx, layout, tin, tout, rot):
+    """A result of more than 256 MB is stored another way: the same bytes as in parts."""
+    heads, dim = 16, 128
+    tokens = (256 << 20) // (heads * dim * torch.finfo(tout).bits // 8) + 77
+    x = torch.randn((tokens, heads, dim), generator=torch.Generator(device="cuda:0").manual_seed(85), device="cuda:0").to(tin)
+    pos, table = torch.arange(tokens, device="cuda:0").remainder(300).to(torch.int32), ctx.rope_table(300, rot)
+    got = ctx.rope(x, pos, table, layout, out_dtype=tout)
+    for a in range(0, tokens, tokens // 3):
+        b = min(a + tokens // 3, tokens)
+        assert torch.equal(got[a:b], ctx.rope(x[a:b], pos[a:b], table, layout, out_dtype=tout))
+
+
+@pytest.mark.parametrize("bits,dtype", [(8, torch.bfloat16), (4, torch.bfloat16), (4, torch.float32)])
+def test_reads_past_the_caches(ctx, bits, dtype):
+    heads, dim, page = 4, 128, 64
+    tokens = (256 << 20) // (2 * heads * dim * torch.finfo(dtype).bits // 8) + 77
+    cache = ctx.kv_cache(40, heads, dim, bits, page)
+    x = torch.randn((40 * page, 2 * heads, dim), generator=torch.Generator(device="cuda:0").manual_seed(86), device="cuda:0")
+    ctx.kv_write(cache, x[:, :heads], x[:, heads:], torch.arange(40 * page, dtype=torch.int32, device="cuda:0"))
+    slots = torch.randint(-1, 40 * page, (tokens,), generator=torch.Generator().manual_seed(87)).to(torch.int32).cuda()
+    got = ctx.kv_read(cache, slots, dtype)
+    for a in range(0, tokens, tokens // 3):
+        b = min(a + tokens // 3, tokens)
+        for whole, part in zip(got, ctx.kv_read(cache, slots[a:b], dtype)):
+            assert torch.equal(whole[a:b], part)
