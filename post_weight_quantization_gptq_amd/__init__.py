@@ -631,12 +631,15 @@ class Context:
                 t.record_stream(self.stream)
 
     def _empty(self, shape, dtype, elsewhere=None):
-        """An output tensor whose memory belongs to the context's stream."""
+        """An output tensor whose memory belongs to the context's stream.  With another torch stream current, the
+        caller's, it counts as used there too: once freed it is not handed out again before what that stream has of it."""
         torch = self.torch
         if not (self._elsewhere() if elsewhere is None else elsewhere):
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
 
     def _plain(self, t, dtype, shape, name):
         """t as a contiguous tensor of the given type and shape on the context's device."""

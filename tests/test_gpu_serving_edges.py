@@ -285,3 +285,34 @@ def test_reads_past_the_caches(ctx, bits, dtype):
         b = min(a + tokens // 3, tokens)
         for whole, part in zip(got, ctx.kv_read(cache, slots[a:b], dtype)):
             assert torch.equal(whole[a:b], part)
+
+
+# ------------------------------------------------------------------ streams --
+def test_results_read_on_the_callers_stream(ctx):
+    """A context on a stream of its own: memory of a result that the caller's stream has yet to read, freed by the caller,
+    is not the next call's result."""
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        own = Context("cuda:0")
+    try:
+        here = torch.cuda.current_stream()
+        x = torch.randn((4096, 8, 64), generator=torch.Generator().manual_seed(97)).cuda()
+        pos, table = i32(np.arange(4096) % 100), own.rope_table(100, 64)
+        y, kept, read = -x, torch.empty_like(x), torch.cuda.Event()
+        kept.copy_(x)
+        side.wait_stream(here)
+        a = own.rope(x, pos, table)
+        here.wait_stream(side)
+        torch.cuda._sleep(50_000_000)  # the caller's stream is some milliseconds behind
+        kept.copy_(a)
+        read.record(here)
+        at = a.data_ptr()
+        del a
+        b = own.rope(y, pos, table)
+        assert b.data_ptr() != at or read.query()  # (a slow host: the read is done)
+        here.wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(kept, -b)
+    finally:
+        torch.cuda.synchronize()
+        own.close()
