@@ -170,7 +170,10 @@ __device__ __forceinline__ int ceil_div(int a, int b) {
 // the fewest tiles for each, at least LEAST, such that no more of them (p.fit for
 // a key head and row block) are made than run at once.  The longest
 // share is what a call takes: eight trees over 0 to 4093 positions 43 us, 47
-// with equally many shares for each sequence.  The whole wave takes part.
+// with equally many shares for each sequence.  The whole wave takes part.  Every
+// workgroup reads all lengths, 64 at a time and up to eight times, which grows with
+// the square of the sequences: calls of 32, 128, 256, 512 and 1024 sequences without
+// positions (8 heads, one token) take 5, 13, 29, 79 and 246 us.
 template <int TP, int LEAST>
 __device__ __forceinline__ bool find_share(const AttnProb& p, int unit, Share& o) {
   static_assert(LEAST * TP >= 256, "the host's bounds count shares of 256 positions or more");
@@ -547,9 +550,10 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 //
 // Up to 16 rows it is bound by reading the codes: 32 contexts of 4096 to 8192
 // tokens, 8 heads of 128 at 8 bits, 423 MB in 85 us, 5.0 TB/s, what a large copy
-// moves; 64 positions a tile, so that 17 KB a wave are on their way.  With more
+// moves (at 4 bits 220 MB in 65 us, vector
+// instructions issued 55% of the time, 38% at 8: unpacking does not halve); 64 positions a tile, so that 17 KB a wave are on their way.  With more
 // rows by its vector instructions, about ten for a score and two for a code: 40
-// rows of 131071 positions, 4 heads at 4 bits, 38 us, issued 55% of the time;
+// rows of 131071 positions, 4 heads at 4 bits, 39 us, issued 56% of the time;
 // 32 positions a tile, so that two waves fit a SIMD without spills.
 template <int DIM, int BITS, int NB, int TP, int WV, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void k_tree_attn(const AttnProb p) {
@@ -848,7 +852,7 @@ __global__ __launch_bounds__(64 * WV, OCC) void k_tree_attn(const AttnProb p) {
 // the workgroup.  The operand layout is that of k_tree_attn with dimension 32
 // ks + 8 g + e in step ks.  Bound by vector instructions (issued 50% of the
 // time) and the waits between them: 108 rows of 0 to 4093 positions, 64 heads of
-// 128 in all at 4 bits, 37 us; 9.9 GFLOP.
+// 128 in all at 4 bits, 38 us; 9.9 GFLOP.
 template <int DIM, int BITS, int NB, int TP>
 __global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
   typedef Tile<DIM, BITS, TP> T;
@@ -1048,8 +1052,8 @@ __global__ __launch_bounds__(256, 2) void k_tree_attn_wide(const AttnProb p) {
 }
 
 // The shares of every row, where a launch of its own joins them: bound by
-// reading them (13824 rows of up to 11 shares of 128 dimensions 7.8 us, 7 TB/s
-// from the last-level cache) or by its latency (160 rows of 64 shares 5.6 us).
+// reading them (13824 rows of up to 11 shares of 128 dimensions 7.5 us, 7 TB/s
+// from the last-level cache) or by its latency (160 rows of 64 shares 5.8 us).
 template <int G>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnProb p) {
   __shared__ JoinLds<G> s;
