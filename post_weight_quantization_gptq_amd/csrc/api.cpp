@@ -1576,6 +1576,7 @@ GPTQ_API int gptq_tree_attention(gptq_ctx c, const gptq_kv_cache* cache, const u
   // saves the second launch (1000 positions, 8 heads of 4 rows: 14.3 against
   // 17.3 us a call).  Where that workgroup would join many rows alone, a launch
   // that fills the chip is faster (108 rows of 4000 positions: 45 against 54 us).
+  // The number of shares is the expected one: the lengths are on the device.
   const bool split = p.most > 1, fuse = split && p.shares <= 8 && p.nb == 1 && !p.wide;
   {
     const size_t rows = split ? (size_t)p.kept * tokens * p.group : 0;

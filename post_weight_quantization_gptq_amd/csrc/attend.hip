@@ -533,10 +533,9 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 //
 // Weights enter the second product times their position's scale, as two
 // bfloat16 numbers, the nearest to it and the nearest to what is left, within 2^-16
-// of it and without a bias: with one of them the weights' rounding would be as large
-// as the result's, and float16's range
-// would lose the weights under 2^-29 of the largest, which are all there is
-// where the others' values are zero.
+// of it and without a bias: with one of them the weights' rounding would be as
+// large as the result's, and float16's range would lose the weights under 2^-29 of
+// the largest, which are all there is where the others' values are zero.
 //
 // In a tile that reaches past the context or a page outside the pool,
 // invisible positions are taken out of scores and weights by selection,
@@ -550,11 +549,11 @@ __device__ __forceinline__ void put_rows(const AttnProb& p, const Rows<NB, NO>& 
 //
 // Up to 16 rows it is bound by reading the codes: 32 contexts of 4096 to 8192
 // tokens, 8 heads of 128 at 8 bits, 423 MB in 85 us, 5.0 TB/s, what a large copy
-// moves (at 4 bits 220 MB in 65 us, vector
-// instructions issued 55% of the time, 38% at 8: unpacking does not halve); 64 positions a tile, so that 17 KB a wave are on their way.  With more
-// rows by its vector instructions, about ten for a score and two for a code: 40
-// rows of 131071 positions, 4 heads at 4 bits, 39 us, issued 56% of the time;
-// 32 positions a tile, so that two waves fit a SIMD without spills.
+// moves (at 4 bits 220 MB in 65 us, vector instructions issued 55% of the time, 38%
+// at 8: unpacking does not halve); 64 positions a tile, so that 17 KB a wave are on
+// their way.  With more rows by its vector instructions, about ten for a score and
+// two for a code: 40 rows of 131071 positions, 4 heads at 4 bits, 39 us, issued 56%
+// of the time; 32 positions a tile, so that two waves fit a SIMD without spills.
 template <int DIM, int BITS, int NB, int TP, int WV, int OCC>
 __global__ __launch_bounds__(64 * WV, OCC) void k_tree_attn(const AttnProb p) {
   typedef Tile<DIM, BITS, TP> T;
