@@ -475,6 +475,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
     walk();
     if (cur == c0 && rounds == r0) break;  // the walk is over where the sum was
     if (a.launch < a.launches - 1) {
+      __syncthreads();  // the walk's nodes are one thread's: other waves may be here before it
       if (tid < T) a.path[b * T + tid] = s.path[tid];
       if (tid == 0) *state = VerifyState{mass, times, cur, rounds, taken, i, 0, 0};
       return;
