@@ -502,11 +502,12 @@ int gptq_probabilities(gptq_ctx ctx, const void* logits, int32_t type, int64_t s
  * on from it; otherwise r = max(r - R Q, 0) and R = sum r (without Q the test is
  * uniforms[b][i] R < r(x), then R -= r(x), r(x) = 0).  Where no child is accepted,
  * next[b] is the first v at which the sum of r up to v passes uniforms[b][0] times
- * the whole (the last v with r > 0 if none does; r = P[b][c] if nothing is left of
- * it; -1 if that is empty).  path[b]: the nodes of the walk from 0 on, then -1;
- * counts[b]: how many.  64-bit sums.  Probabilities below 0 or NaN count as 0; a
- * drafted token outside the vocabulary is not there.  tokens at most 1024, vocab
- * at most 2^20 (GPTQ_ERR_UNSUPPORTED).  Needs workspace, as gptq_tree_attention. */
+ * the whole (the last v with r > 0 if none does, as with a number from 1 on or NaN;
+ * r = P[b][c] if nothing is left of it; -1 if that is empty).  path[b]: the nodes of
+ * the walk from 0 on, then -1; counts[b]: how many.  64-bit sums.  Probabilities below
+ * 0 or NaN count as 0; a drafted token outside the vocabulary is not there.  tokens at
+ * most 1024, vocab at most 2^20 (GPTQ_ERR_UNSUPPORTED).  Needs workspace, as
+ * gptq_tree_attention. */
 int gptq_verify_draft(gptq_ctx ctx, const float* P, int64_t p_seq, int64_t p_token, const float* Q, int64_t q_seq,
                       int64_t q_token, int32_t seqs, int32_t tokens, int32_t vocab, const int32_t* draft,
                       const int32_t* parents, const float* uniforms, int32_t* path, int32_t* counts, int32_t* next);

@@ -489,8 +489,11 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
     sums(0, 1);
     whole = total();
   }
-  const double pass = (double)s.u[0] * whole;
-  // the first tile whose sum passes, then within it; none: the last value there is
+  // From 1 on no sum passes, said here since the sums below are added in another order than
+  // the whole: one may be a last bit larger.
+  const double pass = s.u[0] >= 1.f ? (double)INFINITY : (double)s.u[0] * whole;
+  // the first tile that holds anything and whose sum passes, then within it; none: the
+  // last value there is
   int t = -1, end = -1;
   double before = 0.0;
   for (int t0 = 0; t0 < ntile && t < 0; t0 += 64) {
@@ -501,7 +504,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
       const double y = __shfl_up(x, o);
       if (lane >= o) x += y;
     }
-    const uint64_t past = __ballot(before + x > pass), some = __ballot(v > 0.0);
+    const uint64_t past = __ballot(v > 0.0 && before + x > pass), some = __ballot(v > 0.0);
     if (some) end = t0 + 63 - __builtin_clzll(some);
     if (past) t = t0 + __builtin_ctzll(past);
     before += __shfl(past ? x - v : x, past ? __builtin_ctzll(past) : 63);

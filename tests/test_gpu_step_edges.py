@@ -55,3 +55,31 @@ def test_verify_walks_of_more_than_a_wave(ctx, tokens, vocab, rejected):
     for _ in range(3):
         want = check_verify(ctx, c)
     assert want[1][0] == tokens - len(rejected)
+
+
+def whole_sum_case(g, seqs, tokens, vocab, empty, drawn):
+    """The walk ends at the root, whose children are rejected (of their token p holds nothing)."""
+    p, q = (softmax(g.standard_normal((seqs, tokens, vocab))) for _ in range(2))
+    if empty:  # the last values, and some whole tiles between, hold nothing
+        p[:, :, -empty:] = 0.0
+        p[:, :, 4096:8192] = 0.0
+    draft = np.zeros((seqs, tokens), np.int64)
+    draft[:, 1:] = 5000
+    p[:, :, 5000] = 0.0
+    parents = np.zeros((seqs, tokens), np.int64)
+    parents[:, 0] = -1
+    return dict(p=p, q=q if drawn else None, draft=draft, parents=parents if drawn else None)
+
+
+@pytest.mark.parametrize("seqs,tokens,vocab", [(9, 1, 20000), (9, 2, 20481), (7, 1, 53000), (5, 3, 131072), (3, 2, 270001),
+                                               (40, 2, 50003), (260, 1, 24577)])
+@pytest.mark.parametrize("empty", [0, 1, 9000])
+def test_verify_no_sum_passes_the_whole(ctx, seqs, tokens, vocab, empty):
+    """With a random number of 1 or more no sum passes: the last value with r > 0, however the sums round."""
+    g = np.random.default_rng(seqs + vocab + empty)
+    u = np.full((seqs, tokens), 0.9999, np.float32)
+    for drawn in (False, True):
+        c = whole_sum_case(g, seqs, tokens, vocab, empty, drawn)
+        for u0 in (1.0, 1.5, float("inf"), float("nan"), 1 - 2.0 ** -24, -0.5):
+            u[:, 0] = u0
+            check_verify(ctx, dict(c, uniforms=u))
