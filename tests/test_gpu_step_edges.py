@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from post_weight_quantization_gptq_amd import Context  # noqa: E402
-from test_gpu_step import check_verify  # noqa: E402
+from test_gpu_step import check_verify, draft_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,34 @@ def test_verify_no_sum_passes_the_whole(ctx, seqs, tokens, vocab, empty):
         for u0 in (1.0, 1.5, float("inf"), float("nan"), 1 - 2.0 ** -24, -0.5):
             u[:, 0] = u0
             check_verify(ctx, dict(c, uniforms=u))
+
+
+def rejected_siblings(g, seqs, tokens, vocab):
+    """Trees whose root has all other nodes as children: those of odd sequences are rejected up to a few, those of even
+    ones to the last, each by a residual that a sum over the vocabulary gives."""
+    p = softmax(g.standard_normal((seqs, tokens, vocab)))
+    q = softmax(g.standard_normal((seqs, tokens, vocab)))
+    parents = np.zeros((seqs, tokens), np.int64)
+    parents[:, 0] = -1
+    draft, u = np.zeros((seqs, tokens), np.int64), np.full((seqs, tokens), 0.999, np.float32)
+    below = np.argsort(p[:, 0].astype(np.float64) - q[:, 0], -1)
+    draft[:, 1:] = below[:, :tokens - 1]
+    for b in range(1, seqs, 2):
+        draft[b, b % tokens or 1:] = below[b, -1]
+    u[:, 0] = g.random(seqs)
+    return dict(p=p, q=q, draft=draft, parents=parents, uniforms=u)
+
+
+# fewer workgroups a sequence than tiles (6 of 13, 1 of 10, 32 of 33, 12 of 32), and sums left to the last one of more
+# tiles than it adds at a time
+@pytest.mark.parametrize("seqs,tokens,vocab", [(40, 3, 50003), (130, 2, 40001), (257, 2, 9000), (8, 5, 131073), (21, 4, 131072),
+                                               (4, 12, 50003), (3, 20, 36864), (2, 11, 69633), (300, 9, 4500)])
+def test_verify_several_tiles_a_workgroup(ctx, seqs, tokens, vocab):
+    want = check_verify(ctx, rejected_siblings(np.random.default_rng(seqs + vocab), seqs, tokens, vocab))
+    assert (want[1][::2] == 1).all()
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_of_a_served_batch(ctx, tree, drawn):
+    check_verify(ctx, draft_case(np.random.default_rng(46), 70, 5, 33001, tree, drawn))
