@@ -219,6 +219,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   l = sums[tid & (NT / 64 - 1)];
 #pragma unroll
   for (int o = NT / 128; o > 0; o >>= 1) join(__shfl_xor(m, o), __shfl_xor(l, o));
+  // One lane's sum for all (that of each wave's first lane is the same): one product of a join is
+  // rounded and the other is not, so that two lanes that joined each other differ by a last
+  // bit, and equal logits would not have equal probabilities.
+  l = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, l)));
   m = base(m);
   const float scale = l > 0.f ? 1.f / l : l;  // of -infinity alone 0
   each([&](const Raw<T>& a, int v0, bool whole) {

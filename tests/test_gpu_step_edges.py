@@ -114,3 +114,24 @@ def test_verify_several_tiles_a_workgroup(ctx, seqs, tokens, vocab):
 @pytest.mark.parametrize("drawn", [True, False])
 def test_verify_of_a_served_batch(ctx, tree, drawn):
     check_verify(ctx, draft_case(np.random.default_rng(46), 70, 5, 33001, tree, drawn))
+
+
+# ------------------------------------------------------- probabilities --
+# a row for every kernel: 256 threads; 1024 with 4, 8, 16 and 32 times four values each; block by block
+ROWS = [1000, 4096, 16000, 16384, 32768, 50001, 65536, 100003, 131072, 131073, 270001]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", ROWS)
+def test_equal_logits_have_equal_probabilities(ctx, vocab, dtype):
+    """Wherever they are in the row, the largest in one place."""
+    g = torch.Generator().manual_seed(vocab)
+    values = torch.randn((9, 7), generator=g).to(dtype)
+    values[:, 0] = values.amax(1) + 0.37
+    which = torch.randint(1, 7, (9, vocab), generator=g)
+    which[torch.arange(9), torch.randint(0, vocab, (9,), generator=g)] = 0
+    x = values.gather(1, which)
+    p = ctx.probabilities(x.cuda(), torch.linspace(0.3, 2.0, 9).cuda()).cpu()
+    for b in range(9):
+        for v in range(7):
+            assert p[b, which[b] == v].unique().numel() == 1
