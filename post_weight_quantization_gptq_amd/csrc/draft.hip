@@ -16,7 +16,7 @@ __device__ __forceinline__ void load_any(const float* p, float* o) {
 }  // namespace
 
 // ---------------------------------------------------------- probabilities --
-// p_v = exp((l_v - max) / t) / sum, fp32, as powers of two of (l - max) fl(log2(e) / t);
+// p_v = exp((l_v - max) / t) / sum, fp32, as powers of two of (l - max) s fl(log2(e) / (s t));
 // t = 0: 1 at the first maximum.  A row with a NaN or +infinity (t > 0), or a
 // temperature below 0 or not finite, is NaN; a row of -infinity alone is zero.
 // A workgroup has a row, which stays in its registers from the load on: 4 C values a
@@ -79,8 +79,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   float* y = p.y + b * p.ys + t * p.yt;
   const float warm = p.warm ? p.warm[b] : 1.f;
   const bool greedy = warm == 0.f, fair = warm >= 0.f && warm <= 3.402823466e38f;
-  // held finite: where the reciprocal would not be, all but the maximum vanishes
-  const float c = fminf(1.4426950408889634f / warm, 3.402823466e38f);
+  // Logits are made smaller by a power of two first, half of them or about 1 / t: the
+  // difference of two of any size is finite, and the factor below no smaller than log2(e) / 4.
+  // It is held finite: where it would not be, all but the maximum vanishes.
+  const int down = min(max((int)(__builtin_bit_cast(uint32_t, warm) >> 23 & 255) - 127, 1), 126);
+  const float half = __builtin_bit_cast(float, (127 - down) << 23);
+  const float c = fminf(1.4426950408889634f / (warm * half), 3.402823466e38f);
   constexpr int ROW = 4 * NT, BLOCK = C * ROW;
   auto store = [&](const float* a, int v0, bool whole) {
     const int v = v0 + 4 * tid;
@@ -166,18 +170,19 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   // where that grows.  A NaN, or infinity less infinity, makes it NaN.
   float m = -INFINITY, l = 0.f;
   auto base = [](float m) { return m == -INFINITY ? 0.f : m; };
+  auto power = [&](float v, float from) { return __builtin_amdgcn_exp2f(fmaf(v, half, -from) * c); };
   auto take = [&](const Raw<T>* a, auto n) {
     float top = m;
 #pragma unroll
     for (int k = 0; k < decltype(n)::value; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, a[k].get(i));
-    const float from = base(top);
-    l *= __builtin_amdgcn_exp2f((m - from) * c);
+    const float from = base(top) * half;
+    l *= power(m, from);
 #pragma unroll
     for (int k = 0; k < decltype(n)::value; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l += __builtin_amdgcn_exp2f((a[k].get(i) - from) * c);
+      for (int i = 0; i < 4; ++i) l += power(a[k].get(i), from);
     m = top;
   };
   std::integral_constant<int, 1> one;
@@ -204,8 +209,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   // all loads are back by now; said here, or the stores below would wait for one another
   __builtin_amdgcn_s_waitcnt(VmWait<0>::value);
   auto join = [&](float m2, float l2) {
-    const float top = fmaxf(m, m2), from = base(top);
-    l = l * __builtin_amdgcn_exp2f((m - from) * c) + l2 * __builtin_amdgcn_exp2f((m2 - from) * c);
+    const float top = fmaxf(m, m2), from = base(top) * half;
+    l = l * power(m, from) + l2 * power(m2, from);
     m = top;
   };
 #pragma unroll
@@ -223,12 +228,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   // rounded and the other is not, so that two lanes that joined each other differ by a last
   // bit, and equal logits would not have equal probabilities.
   l = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, l)));
-  m = base(m);
+  m = base(m) * half;
   const float scale = l > 0.f ? 1.f / l : l;  // of -infinity alone 0
   each([&](const Raw<T>& a, int v0, bool whole) {
     float q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_exp2f((a.get(i) - m) * c) * scale;
+    for (int i = 0; i < 4; ++i) q[i] = power(a.get(i), m) * scale;
     store(q, v0, whole);
   });
 }

@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from post_weight_quantization_gptq_amd import Context  # noqa: E402
-from test_gpu_step import check_verify, draft_case  # noqa: E402
+from test_gpu_step import check_probabilities, check_verify, draft_case, up  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,15 @@ def test_equal_logits_have_equal_probabilities(ctx, vocab, dtype):
     for b in range(9):
         for v in range(7):
             assert p[b, which[b] == v].unique().numel() == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [2, 1000, 20000, 70000, 140000])
+def test_probabilities_of_logits_far_apart(ctx, vocab, dtype):
+    """Logits whose difference is past the largest number, temperatures that bring it back, and the smallest ones."""
+    most = float(torch.finfo(dtype).max)
+    x = (torch.linspace(-1, 1, vocab, dtype=torch.float64) * most).to(dtype)[torch.randperm(vocab)]
+    x = torch.stack([x, x / 2, x * 2.0 ** -100, x * 2.0 ** -127, x * 0 + most, -x.abs()])[:, None]
+    for t in (3.4e38, 1e38, 3e37, 1e36, 1e8, 2.0, 1.9, 1e-30, 1.2e-38, 1e-40):
+        temp = torch.full((6,), t)
+        check_probabilities(ctx.probabilities(x.cuda(), temp.cuda()), up(x), temp.numpy())
