@@ -16,7 +16,7 @@ __device__ __forceinline__ void load_any(const float* p, float* o) {
 }  // namespace
 
 // ---------------------------------------------------------- probabilities --
-// p_v = exp((l_v - max) / t) / sum, fp32, as powers of two of (l - max) s fl(log2(e) / (s t));
+// p_v = exp((l_v - max) / t) / sum, fp32, as powers of two of (l - max) log2(e) / t;
 // t = 0: 1 at the first maximum.  A row with a NaN or +infinity (t > 0), or a
 // temperature below 0 or not finite, is NaN; a row of -infinity alone is zero.
 // A workgroup has a row, which stays in its registers from the load on: 4 C values a
@@ -52,6 +52,11 @@ struct Raw {  // four values of a row
   }
 };
 
+// The first lane's.
+__device__ __forceinline__ float all_lanes(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+
 template <int NT, class F>
 __device__ __forceinline__ float over_all(float x, float* part, F&& f) {
 #pragma unroll
@@ -81,10 +86,16 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   const bool greedy = warm == 0.f, fair = warm >= 0.f && warm <= 3.402823466e38f;
   // Logits are made smaller by a power of two first, half of them or about 1 / t: the
   // difference of two of any size is finite, and the factor below no smaller than log2(e) / 4.
-  // It is held finite: where it would not be, all but the maximum vanishes.
+  // It is held finite: where it would not be, all but the maximum vanishes.  The factor is two
+  // numbers: one is off by up to 2^-24 of itself, which a value d below the largest has d / t
+  // times.  The first is below the factor, so that the second is above 0: times -infinity it
+  // must not be NaN.  What the first leaves of log2(e) is exact but for its own last bit.
   const int down = min(max((int)(__builtin_bit_cast(uint32_t, warm) >> 23 & 255) - 127, 1), 126);
   const float half = __builtin_bit_cast(float, (127 - down) << 23);
-  const float c = fminf(1.4426950408889634f / (warm * half), 3.402823466e38f);
+  constexpr float log2e = 1.44269502162933f, log2e_rest = 1.92596299112661e-8f, ln2 = 0.693147180559945f;
+  const float nearest = fminf(log2e / (warm * half), 3.402823466e38f);
+  const float c = all_lanes(__builtin_bit_cast(float, __builtin_bit_cast(int, nearest) - 1));
+  const float rest = all_lanes(fmaxf((fmaf(-c, warm * half, log2e) + log2e_rest) * (c * ln2), 0x1p-100f));
   constexpr int ROW = 4 * NT, BLOCK = C * ROW;
   auto store = [&](const float* a, int v0, bool whole) {
     const int v = v0 + 4 * tid;
@@ -170,7 +181,10 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   // where that grows.  A NaN, or infinity less infinity, makes it NaN.
   float m = -INFINITY, l = 0.f;
   auto base = [](float m) { return m == -INFINITY ? 0.f : m; };
-  auto power = [&](float v, float from) { return __builtin_amdgcn_exp2f(fmaf(v, half, -from) * c); };
+  auto power = [&](float v, float from) {
+    const float d = fmaf(v, half, -from);
+    return __builtin_amdgcn_exp2f(fmaf(d, c, d * rest));
+  };
   auto take = [&](const Raw<T>* a, auto n) {
     float top = m;
 #pragma unroll
@@ -227,7 +241,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
   // One lane's sum for all (that of each wave's first lane is the same): one product of a join is
   // rounded and the other is not, so that two lanes that joined each other differ by a last
   // bit, and equal logits would not have equal probabilities.
-  l = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, l)));
+  l = all_lanes(l);
   m = base(m) * half;
   const float scale = l > 0.f ? 1.f / l : l;  // of -infinity alone 0
   each([&](const Raw<T>& a, int v0, bool whole) {

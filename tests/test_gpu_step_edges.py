@@ -4,10 +4,13 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from oracle import step_ref  # noqa: E402
 from post_weight_quantization_gptq_amd import Context  # noqa: E402
 from test_gpu_step import check_probabilities, check_verify, draft_case, up  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -147,3 +150,48 @@ def test_probabilities_of_logits_far_apart(ctx, vocab, dtype):
     for t in (3.4e38, 1e38, 3e37, 1e36, 1e8, 2.0, 1.9, 1e-30, 1.2e-38, 1e-40):
         temp = torch.full((6,), t)
         check_probabilities(ctx.probabilities(x.cuda(), temp.cuda()), up(x), temp.numpy())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,seqs", [(2, 20000), (3000, 2000), (20000, 500), (40000, 300), (70000, 200), (140000, 100)])
+def test_probabilities_far_below_the_largest(ctx, vocab, seqs, dtype):
+    """Rows of two logits, 0 and -d (exact in both types), the others masked: exp(-d / t) / (1 + exp(-d / t)).
+
+    The exponent d log2(e) / t is rounded once, by half a step, 2^-24 of it: d / t times that in the result.  exp2 is within
+    2^-23, the sum, the quotient and the product within 2^-24 each: 5 of these, 8 with what is left of higher order."""
+    g = torch.Generator().manual_seed(vocab)
+    t = torch.exp(8 * torch.rand(seqs, generator=g) - 4)
+    d = (t * (15 + 70 * torch.rand(seqs, generator=g))).to(dtype)
+    x = torch.full((seqs, 1, vocab), float("-inf"), dtype=dtype)
+    places = torch.stack([torch.randperm(vocab, generator=g)[:2] for _ in range(seqs)])
+    rows = torch.arange(seqs)
+    x[rows, 0, places[:, 0]], x[rows, 0, places[:, 1]] = 0.0, -d
+    p = ctx.probabilities(x.cuda(), t.cuda()).cpu()
+    s = up(d) / up(t)
+    want = np.exp(-s) / (1 + np.exp(-s))
+    err = np.abs(up(p[rows, 0, places[:, 1]]) - want) / want / U
+    print("largest error %.1f of %.1f" % (err.max(), (s + 8).max()), flush=True)
+    assert np.all(err <= s + 8 + 2.0 ** -125 / want / U)
+    assert np.all(np.abs(up(p[rows, 0, places[:, 0]]) - 1 / (1 + np.exp(-s))) <= 8 * U)
+    assert int((p != 0).sum()) == 2 * seqs
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", ROWS)
+def test_probabilities_within_the_roundings(ctx, vocab, dtype):
+    """|error| <= p (k d + k E + n + 3 (n / 16 + 4) + 52) 2^-24 + 2^-125, d = (largest - logit) / t, E its mean over p.
+
+    The exponent is rounded once, 2^-24 d of the result, and the difference of two fp32 logits too (k = 2; of two bf16
+    ones of these sizes it is exact: k = 1).  exp2 is within 2^-23.  The sum has that of its terms, d on average E; a thread
+    adds n of them and makes its sum smaller once for 16 and for each of up to four at the row's end (an exp2 and a
+    product, 3; the exponent's parts add up to d); a tree of 10 levels with an exp2, a product and an addition
+    each, 4; the quotient and the product."""
+    g = torch.Generator().manual_seed(vocab + 1)
+    x = (4.0 * torch.randn((4, 2, vocab), generator=g)).to(dtype)
+    t = torch.tensor([0.3, 0.77, 1.0, 1.9])
+    got, ref = up(ctx.probabilities(x.cuda(), t.cuda())), step_ref.probabilities(up(x), t.numpy())
+    d = (up(x).max(-1, keepdims=True) - up(x)) / up(t)[:, None, None]
+    k, n = (1 if dtype == torch.bfloat16 else 2), -(-vocab // (256 if vocab <= 4096 else 1024))
+    bound = ref * (k * d + k * (ref * d).sum(-1, keepdims=True) + n + 3 * (n / 16 + 4) + 52) * U + 2.0 ** -125
+    print("largest error / bound %.3f" % (np.abs(got - ref) / bound).max(), flush=True)
+    assert np.all(np.abs(got - ref) <= bound)
