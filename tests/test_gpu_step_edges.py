@@ -195,3 +195,24 @@ def test_probabilities_within_the_roundings(ctx, vocab, dtype):
     bound = ref * (k * d + k * (ref * d).sum(-1, keepdims=True) + n + 3 * (n / 16 + 4) + 52) * U + 2.0 ** -125
     print("largest error / bound %.3f" % (np.abs(got - ref) / bound).max(), flush=True)
     assert np.all(np.abs(got - ref) <= bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", ROWS)
+def test_every_value_counts(ctx, vocab, dtype):
+    """One logit far above the others at each border of what a workgroup reads at once: its probability is 1, the others'
+    are exp(-60); left out of the sum or of the largest value it would be any other number."""
+    row = 1024 if vocab <= 4096 else 4096
+    at = sorted({v for c in range(0, vocab + row, row) for v in (c - 1, c, c + 1, c + 3, c + 4)} & set(range(vocab)) | {vocab - 1})
+    x = torch.zeros((1, len(at), vocab), dtype=dtype, device="cuda:0")
+    x[0, torch.arange(len(at)), torch.tensor(at)] = 60.0
+    p = ctx.probabilities(x)[0]
+    top = p[torch.arange(len(at)), torch.tensor(at)].double()
+    assert float((top - 1).abs().max()) <= 8 * U
+    low = torch.where(x[0] == 0, p, np.exp(-60)).double()
+    assert float((low / np.exp(-60) - 1).abs().max()) <= (60 + 8) * U
+    # and one that is not there at all
+    x = torch.where(x == 0, 1.0, float("-inf")).to(dtype)
+    p = ctx.probabilities(x)[0].double()
+    assert bool((p[x[0] == float("-inf")] == 0).all())
+    assert float((p[x[0] == 1] * (vocab - 1) - 1).abs().max()) <= (vocab / 256 + 60) * U
