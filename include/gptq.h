@@ -465,7 +465,7 @@ int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t
  * with What as in gptq_gemm_wqa16 (the same operands and requirements), down
  * [count][rank][K] and up[count][N][rank] bf16 bits, alpha[count] fp32 (NULL: 1),
  * ids[M] int32 (outside 0..count-1: a row without an adapter).  fp32 sums; X down^T
- * enters the second product as two bf16 numbers, within 2^-17 of it.  What a row's
+ * enters the second product as three bf16 numbers, which hold all of it.  What a row's
  * adapter holds reaches no other row.  Rows in any order; those of an adapter side
  * by side are fastest.  rank a multiple of 8, at most 128 (0: the product alone);
  * N at most 2^26; 16-byte aligned rows of X, codes and adapters (GPTQ_ERR_UNSUPPORTED).

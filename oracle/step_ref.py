@@ -14,8 +14,9 @@ def gemm_adapters(X, weights, down, up, ids, alpha=None):
     matrix unit is given them, down [count, r, K], up [count, N, r], ids [M].
 
     bound: K sums in float32 of each product, in any order, are off by at most gamma_K of the sum of magnitudes; X
-    down^T by that, alpha and the shares of K (16 more roundings at most), then as two bf16 numbers by 2^-16 of it
-    (each within half a step, 2^-8 times 2^-8), and the second product's sums over 2 r terms and its addition."""
+    down^T by that, alpha and the shares of K (16 more roundings at most); it is all there in three bf16 numbers (8 bits
+    each, and each one's rounding error has the next one's); then the second product's sums over 3 r terms and its
+    addition."""
     X, weights = np.asarray(X, np.float64), np.asarray(weights, np.float64)
     K = X.shape[1]
 
@@ -31,7 +32,7 @@ def gemm_adapters(X, weights, down, up, ids, alpha=None):
         t, size = f * (d @ X[m]), abs(f) * (np.abs(d) @ np.abs(X[m]))
         Y[m] += u @ t
         part = np.abs(u) @ size
-        bound[m] += (gamma(K + 32) + 2.0 ** -16 + gamma(2 * d.shape[0] + 16)) * 1.01 * part
+        bound[m] += (gamma(K + 32) + gamma(3 * d.shape[0] + 16)) * 1.01 * part
         bound[m] += 16 * U * np.abs(Y[m])
     return Y, bound
 

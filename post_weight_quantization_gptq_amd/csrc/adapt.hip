@@ -66,13 +66,13 @@ __device__ __forceinline__ int id_of(const AdaptProb& p, int row) {
   return (unsigned)a < (unsigned)p.count ? a : -1;
 }
 
-// Eight of a row's alpha T, its shares of k added in order, and as two bf16 numbers,
-// the nearest and the nearest to what is left: within 2^-17 of it, so that the fp32 sums
-// of the second product are not drowned (one bf16 would be off by 2^-9 of the
-// adapter's part).  The first is a finite one: past the largest, and for an infinity or
-// a NaN, the second says the rest.
+// Eight of a row's alpha T, its shares of k added in order, and as three bf16 numbers, the
+// nearest and twice the nearest to what is left: 24 bits, which is all of it (two would be off
+// by 2^-17 of the adapter's part, more than the fp32 sums of the second product).  The
+// first two are finite: past the largest, and for an infinity or a NaN, the last says the
+// rest.
 struct Parts {
-  u32x4 hi, lo;
+  u32x4 part[3];
 };
 __device__ __forceinline__ Parts parts_of(const AdaptProb& p, int row, int at, float alpha) {
   const f32x4* t = (const f32x4*)(p.T + (size_t)row * p.rank + at);
@@ -89,8 +89,10 @@ __device__ __forceinline__ Parts parts_of(const AdaptProb& p, int row, int at, f
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-    v.hi[i] = pack2(__builtin_amdgcn_fmed3f(x, -most, most), __builtin_amdgcn_fmed3f(y, -most, most));
-    v.lo[i] = pack2(x - bf_low(v.hi[i]), y - bf_high(v.hi[i]));
+    v.part[0][i] = pack2(__builtin_amdgcn_fmed3f(x, -most, most), __builtin_amdgcn_fmed3f(y, -most, most));
+    const float x1 = x - bf_low(v.part[0][i]), y1 = y - bf_high(v.part[0][i]);
+    v.part[1][i] = pack2(__builtin_amdgcn_fmed3f(x1, -most, most), __builtin_amdgcn_fmed3f(y1, -most, most));
+    v.part[2][i] = pack2(x1 - bf_low(v.part[1][i]), y1 - bf_high(v.part[1][i]));
   }
   return v;
 }
@@ -271,7 +273,8 @@ __global__ __launch_bounds__(64 * AD_W) void k_adapt_down(const AdaptProb p) {
 template <int BITS, int RB, int CB, int NW>
 __global__ __launch_bounds__(64 * NW) void k_adapt_rows(const AdaptProb p) {
   constexpr int PAIRS = 16 * RB, MINE = (PAIRS + NW - 1) / NW, AT = MINE < 8 ? MINE : 8;
-  constexpr int SUMS = NW * RB * CB * 1024, ROWS = 16 * RB * (4 * 128 + 16);
+  constexpr int SUMS = NW * RB * CB * 1024, ROWS = 16 * RB * (6 * 128 + 16);
+  static_assert(NW % RB == 0, "a wave's pairs are of one group of rows");
   __shared__ __attribute__((aligned(16))) uint8_t lds[SUMS > ROWS ? SUMS : ROWS];  // the rows' T, then the waves' sums
   __shared__ int pa[PAIRS];
   __shared__ uint32_t pm[PAIRS];
@@ -341,14 +344,14 @@ __global__ __launch_bounds__(64 * NW) void k_adapt_rows(const AdaptProb p) {
       }
   };
   Block even, odd;
-  const int per = p.rank >> 3, pitch = 4 * p.rank + 16;  // chunks of eight: of T's first numbers, then of the rests
+  const int per = p.rank >> 3, pitch = 6 * p.rank + 16;  // chunks of eight: of T's first numbers, of the next, of the last
   for (int i = tid; i < PAIRS; i += 64 * NW) pa[i] = -1;
   for (int i = tid; i < 16 * RB * per; i += 64 * NW) {
     const int row = i / per, q = i % per, a = id_of(p, m0 + row);
     if (a < 0) continue;
     const Parts v = parts_of(p, m0 + row, 8 * q, p.alpha ? p.alpha[a] : 1.f);
-    *(u32x4*)(lds + row * pitch + 16 * q) = v.hi;
-    *(u32x4*)(lds + row * pitch + 16 * (per + q)) = v.lo;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) *(u32x4*)(lds + row * pitch + 16 * (e * per + q)) = v.part[e];
   }
   if (b0 < b1) load(even, b0);  // on its way beside the adapters' loads
   __syncthreads();
@@ -377,29 +380,30 @@ __global__ __launch_bounds__(64 * NW) void k_adapt_rows(const AdaptProb p) {
     for (int k = 0; k < AT; ++k)
 #pragma unroll
       for (int n = 0; n < CB; ++n) z[k][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int q0 = 0; q0 < 2 * per; q0 += 4) {
-      const int q = min(q0 + c, 2 * per - 1), r = q < per ? q : q - per;
+    for (int q0 = 0; q0 < per; q0 += 4) {
+      const int q = min(q0 + c, per - 1);
+      const bool there = q0 + c < per;
+      const u32x4 none = {0u, 0u, 0u, 0u};
       // all loads without a branch between them: a pair that is not there reads adapter 0's
-      u32x4 ta[AT], b[AT][CB];
-#pragma unroll
-      for (int k = 0; k < AT; ++k) {
-        ta[k] = *(const u32x4*)(lds + (16 * ((i0 + NW * k) % RB) + j) * pitch + 16 * q);
-#pragma unroll
-        for (int n = 0; n < CB; ++n)
-          b[k][n] = *(const gu32x4*)(p.up + ((size_t)max(pair[k], 0) * p.N + nrow[n]) * p.rank + 8 * r);
-      }
-      if (q0 + c >= 2 * per) {
-#pragma unroll
-        for (int k = 0; k < AT; ++k) {
-          ta[k] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int n = 0; n < CB; ++n) b[k][n] = ta[k];
-        }
-      }
+      u32x4 b[AT][CB];
 #pragma unroll
       for (int k = 0; k < AT; ++k)
 #pragma unroll
-        for (int n = 0; n < CB; ++n) z[k][n] = mma16(ta[k], b[k][n], z[k][n]);
+        for (int n = 0; n < CB; ++n)
+          b[k][n] = *(const gu32x4*)(p.up + ((size_t)max(pair[k], 0) * p.N + nrow[n]) * p.rank + 8 * q);
+#pragma unroll
+      for (int k = 0; k < AT; ++k)
+#pragma unroll
+        for (int n = 0; n < CB; ++n) b[k][n] = there ? b[k][n] : none;
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        u32x4 t = *(const u32x4*)(lds + (16 * (w % RB) + j) * pitch + 16 * (e * per + q));
+        t = there ? t : none;
+#pragma unroll
+        for (int k = 0; k < AT; ++k)
+#pragma unroll
+          for (int n = 0; n < CB; ++n) z[k][n] = mma16(t, b[k][n], z[k][n]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < AT; ++k) {
@@ -465,7 +469,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void k_adapt_tile(co
   constexpr int HALF = (BM + BN) * 64, STAGE = KH * HALF, PER = KH * (NA + NB);
   // rows of products before a stage's barrier; those behind it cover the next stage's reads
   constexpr int BEFORE = AI >= 4 ? AI / 2 : 0;
-  constexpr int RING = NS * STAGE, ROWS = BM * (4 * 128 + 16);
+  constexpr int PITCH = 3 * 8 * 16 + 16, RING = NS * STAGE, ROWS = BM * PITCH;
   static_assert(NA * NW * 16 == BM && NB * NW * 16 == BN, "whole copies");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[RING > ROWS ? RING : ROWS];  // the ring, then the rows' T
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -590,78 +594,77 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 1) void k_adapt_tile(co
     __builtin_amdgcn_s_waitcnt(VmWait<0>::value);  // no copy into LDS outlives the group
   }
 
-  // The adapters' part.  The rows' T goes to LDS as bf16 (the ring is free), 16 bytes more
-  // than a row so that the rows of a read fall on different banks.  For one adapter of
-  // the wave's rows after the other its half is read once for all of them; the products
-  // are from zero on and added to its own rows only: what it holds reaches no other's.
-  // Of several workgroups each takes some of the chunks.
+  // The adapters' part, eight chunks of eight ranks at a time.  The rows' T goes to LDS as bf16
+  // (the ring is free), 16 bytes more than a row so that the rows of a read fall on different
+  // banks.  For one adapter of the wave's rows after the other its half is read once
+  // for all of them; the products are from zero on and added to its own rows only: what it
+  // holds reaches no other's.  Of several workgroups each takes some of the chunks.
   if (p.rank > 0) {
-    const int pitch = 4 * p.rank + 16, per = p.rank >> 3;
-    const int qa = 2 * per * share / parts, qb = 2 * per * (share + 1) / parts;  // this workgroup's chunks
-    __syncthreads();
-    for (int i = threadIdx.x; i < BM * per; i += 64 * NW) {
-      const int row = i / per, q = i % per, a = id_of(p, m0 + row);
-      if (a < 0) continue;
-      const Parts v = parts_of(p, m0 + row, 8 * q, p.alpha ? p.alpha[a] : 1.f);
-      *(u32x4*)(lds + row * pitch + 16 * q) = v.hi;
-      *(u32x4*)(lds + row * pitch + 16 * (per + q)) = v.lo;
-    }
-    __syncthreads();
+    const int per = p.rank >> 3;
+    const int qa = per * share / parts, qb = per * (share + 1) / parts;  // this workgroup's chunks
     constexpr int IH = (WM + 63) / 64;
     int ids[IH];
-    uint64_t open[IH];
 #pragma unroll
-    for (int h = 0; h < IH; ++h) {
-      ids[h] = 64 * h + lane < WM ? id_of(p, m0 + wm0 + 64 * h + lane) : -1;
-      open[h] = __ballot(ids[h] >= 0);
-    }
+    for (int h = 0; h < IH; ++h) ids[h] = 64 * h + lane < WM ? id_of(p, m0 + wm0 + 64 * h + lane) : -1;
 #pragma unroll 1
-    for (;;) {
-      int a = -1;
+    for (int q1 = qa; q1 < qb; q1 += 8) {
+      const int nq = min(8, qb - q1);
+      __syncthreads();
+      for (int i = threadIdx.x; i < BM * nq; i += 64 * NW) {
+        const int row = i / nq, q = i % nq, a = id_of(p, m0 + row);
+        if (a < 0) continue;
+        const Parts v = parts_of(p, m0 + row, 8 * (q1 + q), p.alpha ? p.alpha[a] : 1.f);
 #pragma unroll
-      for (int h = 0; h < IH; ++h)
-        if (a < 0 && open[h]) a = __builtin_amdgcn_readlane(ids[h], __builtin_ctzll(open[h]));
-      if (a < 0) break;
-      uint64_t mine[IH];
-#pragma unroll
-      for (int h = 0; h < IH; ++h) {
-        mine[h] = __ballot(ids[h] == a);
-        open[h] &= ~mine[h];
+        for (int e = 0; e < 3; ++e) *(u32x4*)(lds + row * PITCH + 16 * (8 * e + q)) = v.part[e];
       }
-      // chunks of eight: of T's first numbers, then of the rests, four a product; up to 16
-      // at a time (ranks up to 64), whose loads for all columns are in flight together
+      __syncthreads();
+      uint64_t open[IH];
+#pragma unroll
+      for (int h = 0; h < IH; ++h) open[h] = __ballot(ids[h] >= 0);
 #pragma unroll 1
-      for (int q1 = qa; q1 < qb; q1 += 16) {
-        bf16x8 b[BJ][4];
+      for (;;) {
+        int a = -1;
+#pragma unroll
+        for (int h = 0; h < IH; ++h)
+          if (a < 0 && open[h]) a = __builtin_amdgcn_readlane(ids[h], __builtin_ctzll(open[h]));
+        if (a < 0) break;
+        uint64_t mine[IH];
+#pragma unroll
+        for (int h = 0; h < IH; ++h) {
+          mine[h] = __ballot(ids[h] == a);
+          open[h] &= ~mine[h];
+        }
+        const u32x4 none = {0u, 0u, 0u, 0u};
+        // the loads for all columns are in flight together
+        u32x4 b[BJ][2];
 #pragma unroll
         for (int j = 0; j < BJ; ++j) {
           const int col = min(n0 + wn0 + 16 * j + j16, p.N - 1);
-          const uint16_t* up = p.up + ((size_t)a * p.N + col) * p.rank;
+          const uint16_t* up = p.up + ((size_t)a * p.N + col) * p.rank + 8 * q1;
 #pragma unroll
-          for (int q0 = 0; q0 < 4; ++q0) {
-            const int q = q1 + 4 * q0 + c4;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (q < qb) v = *(const u32x4*)(up + 8 * (q < per ? q : q - per));
-            b[j][q0] = __builtin_bit_cast(bf16x8, v);
+          for (int g = 0; g < 2; ++g) {
+            b[j][g] = none;
+            if (4 * g + c4 < nq) b[j][g] = *(const u32x4*)(up + 8 * (4 * g + c4));
           }
         }
 #pragma unroll
         for (int i = 0; i < AI; ++i) {
           const uint32_t rows = (uint32_t)(mine[i / 4] >> (16 * (i % 4))) & 0xFFFFu;
           if (!rows) continue;  // uniform
-          const uint8_t* t = lds + (wm0 + 16 * i + j16) * pitch;
+          const uint8_t* t = lds + (wm0 + 16 * i + j16) * PITCH + 16 * c4;
           f32x4 z[BJ];
 #pragma unroll
           for (int j = 0; j < BJ; ++j) z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q0 = 0; q0 < 4; ++q0)
-            if (q1 + 4 * q0 < qb) {
-              const int q = q1 + 4 * q0 + c4;
-              u32x4 v = *(const u32x4*)(t + 16 * min(q, qb - 1));
-              if (q >= qb) v = u32x4{0u, 0u, 0u, 0u};
+          for (int g = 0; g < 2; ++g)
+            if (4 * g < nq) {  // uniform
 #pragma unroll
-              for (int j = 0; j < BJ; ++j)
-                z[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), b[j][q0], z[j], 0, 0, 0);
+              for (int e = 0; e < 3; ++e) {
+                u32x4 v = *(const u32x4*)(t + 16 * (8 * e + 4 * g));
+                v = 4 * g + c4 < nq ? v : none;
+#pragma unroll
+                for (int j = 0; j < BJ; ++j) z[j] = mma16(v, b[j][g], z[j]);
+              }
             }
 #pragma unroll
           for (int j = 0; j < BJ; ++j)

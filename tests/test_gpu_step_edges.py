@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import step_ref  # noqa: E402
-from post_weight_quantization_gptq_amd import Context  # noqa: E402
+from post_weight_quantization_gptq_amd import Adapters, Context  # noqa: E402
 from test_gpu_step import check_probabilities, check_verify, draft_case, up  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -216,3 +216,33 @@ def test_every_value_counts(ctx, vocab, dtype):
     p = ctx.probabilities(x)[0].double()
     assert bool((p[x[0] == float("-inf")] == 0).all())
     assert float((p[x[0] == 1] * (vocab - 1) - 1).abs().max()) <= (vocab / 256 + 60) * U
+
+
+# ------------------------------------------------------------- adapters --
+# few rows (16, 32, 64, 128, 128 of many outputs), then a size for every tile, 64 x 64 by one and by several workgroups
+KERNELS = [(3, 40, 32), (30, 200, 64), (60, 333, 160), (100, 500, 32), (128, 2100, 96), (200, 700, 64), (200, 700, 2048),
+           (500, 4090, 1280), (700, 3000, 32), (2000, 3800, 32), (2500, 4000, 32)]
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 72, 128])
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_adapters_in_full(ctx, M, N, K, rank):
+    """alpha X down^T enters the second product with all its bits: weights of 0, one rank and one input that are not 0,
+    so that Y = alpha up, three exact parts added up, each addition within a step of 2^-23 however it rounds."""
+    g = torch.Generator().manual_seed(M + rank)
+    count = 31
+    X = torch.zeros((M, K), dtype=torch.bfloat16)
+    X[:, 5] = 1.0
+    down = torch.zeros((count, rank, K), dtype=torch.bfloat16)
+    which = torch.arange(count) * 5 % rank
+    down[torch.arange(count), which, 5] = 1.0
+    upw = torch.randn((count, N, rank), generator=g).to(torch.bfloat16)
+    alpha = torch.randn(count, generator=g)
+    ids = torch.randint(-1, count, (M,), generator=g, dtype=torch.int32)
+    q = torch.zeros((N, K // 8), dtype=torch.int32), torch.zeros((N, 1)), torch.zeros((N, 1), dtype=torch.uint8)
+    Y = ctx.gemm_adapters(X.cuda(), *(t.cuda() for t in q), 0, 4, Adapters(down.cuda(), upw.cuda(), alpha.cuda()), ids.cuda())
+    a = ids.clamp(min=0).long()
+    want = alpha.double()[a, None] * upw.double()[a, :, which[a]] * (ids >= 0)[:, None]
+    err = (Y.cpu().double() - want).abs()
+    print("largest error %.2f of 6" % float((err / want.abs().clamp(min=1e-30)).max() / U), flush=True)
+    assert bool((err <= 6 * U * want.abs()).all())
