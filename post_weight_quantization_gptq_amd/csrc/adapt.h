@@ -3,7 +3,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-struct AdaptProb {
+#include "adapt_plan.h"
+
+struct AdaptProb : AdaptPlan {
   const uint16_t* X;  // bf16 bits, row pitch ldx
   const uint32_t* P;  // [N][K bits / 32] row bitstreams
   const float* S;     // [N][G]
@@ -22,16 +24,8 @@ struct AdaptProb {
   int M, N, K, G;
   int gshift;  // group = 2^gshift (31: one group a row)
   int count, rank;
-  int shape;  // of the product: 0 few rows, 1 .. 5 its tiles
-  int parts;  // workgroups of a tile, shapes 1 and 2
   int wdown, wrows;  // workgroups of the first launch's first two kinds
-  int splits, slots;  // of the first launch: shares of k, workgroups for the adapters of the same 32 rows
 };
 
-// Which kernels (shape, splits, slots).
-void plan_adapt(AdaptProb& p, int ncu);
-// Bytes that parts > 1 needs for the sums and for the counts.
-size_t adapt_part(const AdaptProb& p);
-size_t adapt_done(const AdaptProb& p);
 hipError_t launch_adapt_down(const AdaptProb& p, int bits, hipStream_t st);
 hipError_t launch_adapt_product(const AdaptProb& p, int bits, hipStream_t st);

@@ -1646,10 +1646,10 @@ GPTQ_API int gptq_gemm_adapters(gptq_ctx c, const uint16_t* X, int64_t M, int64_
     p.X = X + m * ldx;
     p.ids = ids + m;
     p.Y = Y + m * ldy;
-    plan_adapt(p, c->ncu);
+    static_cast<AdaptPlan&>(p) = plan_adapt(p.M, N, K, c->ncu);
     // X in blocks for few rows, the weights in blocks for many, X down^T
     const size_t blocks = (p.shape ? (size_t)cdiv(N, 16) * 16 * K : (size_t)cdiv(p.M, 16) * 16 * cdiv(K, 128) * 128) * sizeof(uint16_t);
-    const size_t sums = adapt_part(p), done = adapt_done(p);
+    const size_t sums = adapt_part(p, p.M, N), done = adapt_done(p, p.M, N);
     int rc = ensure_kept(c, c->adapt, blocks + sums + (size_t)p.splits * p.M * p.rank * sizeof(float));
     if (!rc && done) rc = ensure_kept(c, c->counts, done, true);
     if (rc) return rc;

@@ -6,7 +6,8 @@ torch = pytest.importorskip("torch")
 
 from oracle import step_ref  # noqa: E402
 from post_weight_quantization_gptq_amd import Adapters, Context  # noqa: E402
-from test_gpu_step import check_probabilities, check_verify, draft_case, up  # noqa: E402
+from test_gpu_step import (adapters_of, check_adapters, check_probabilities, check_verify, draft_case, f32, i32,  # noqa: E402
+                           layer, rows_of, up)
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +247,58 @@ def test_adapters_in_full(ctx, M, N, K, rank):
     err = (Y.cpu().double() - want).abs()
     print("largest error %.2f of 6" % float((err / want.abs().clamp(min=1e-30)).max() / U), flush=True)
     assert bool((err <= 6 * U * want.abs()).all())
+
+
+LARGE = KERNELS[7:]  # 128 x 128 by two workgroups and by one, 128 x 256, 256 x 256
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_rows_in_any_order_on_every_tile(ctx, M, N, K):
+    """Rows and results of pitched tensors, sixteen rows of an operand with up to as many adapters."""
+    q, w = layer(N, K, 32, 4, 5)
+    ad, down, upw, alpha = adapters_of(11, 24, K, N, 6)
+    wide = torch.full((M, K + 8), float("nan"), dtype=torch.bfloat16)
+    wide[:, :K] = rows_of(M, K, 7)
+    ids = np.random.default_rng(8).integers(-1, 11, M)
+    Y = torch.full((M, N + 3), 7.0, device="cuda:0")
+    got = ctx.gemm_adapters(wide.cuda()[:, :K], *q, 32, 4, ad, i32(ids), Y=Y[:, :N])
+    assert bool((Y[:, N:] == 7.0).all())
+    rows = np.unique(np.r_[0:140, M // 2:M // 2 + 70, M - 70:M])
+    check_adapters(got[torch.from_numpy(rows).cuda()], wide[rows, :K], w, down, upw, ids[rows], alpha)
+
+
+@pytest.mark.parametrize("sort", [False, True])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_an_adapter_reaches_its_own_rows_on_every_tile(ctx, M, N, K, sort):
+    """NaN and infinity in one adapter, and in one row of X, change no other row by a bit."""
+    q, _ = layer(N, K, 0, 4, 1)
+    ad, *_ = adapters_of(5, 24, K, N, 2)
+    X = rows_of(M, K, 3).cuda()
+    ids = np.random.default_rng(4).integers(-1, 5, M)
+    if sort:
+        ids.sort()
+    mine = np.nonzero(ids == 1)[0]
+    row = int(mine[len(mine) // 2])
+    want = ctx.gemm_adapters(X, *q, 0, 4, ad, i32(ids))
+    ad.down[2, 3, 5], ad.up[2, 7, 1], ad.up[2, 9] = float("nan"), float("inf"), float("nan")
+    ad.alpha[2] = float("inf")
+    X[row, 17] = float("nan")
+    got = ctx.gemm_adapters(X, *q, 0, 4, ad, i32(ids))
+    others = torch.from_numpy((ids != 2) & (np.arange(M) != row)).cuda()
+    assert torch.equal(got[others], want[others])
+    assert bool(got[torch.from_numpy(ids == 2).cuda()].isnan().any(1).all()) and bool(got[row].isnan().all())
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_adapters_past_the_largest_bf16_on_every_tile(ctx, M, N, K):
+    q, w = layer(N, K, 0, 4, 25)
+    X = torch.zeros((M, K), dtype=torch.bfloat16)
+    X[:, 0] = 1.0
+    down = torch.zeros((2, 8, K), dtype=torch.bfloat16)
+    down[:, :, 0] = 1.0
+    upw = ((0.5 + torch.rand((2, N, 8), generator=torch.Generator().manual_seed(26))) * 2.0 ** -100).to(torch.bfloat16)
+    ids = np.arange(M) % 3 - 1
+    got = ctx.gemm_adapters(X.cuda(), *q, 0, 4, Adapters(down.cuda(), upw.cuda(), f32([3.4e38, float("inf")])), i32(ids))
+    assert bool(torch.isposinf(got[torch.from_numpy(ids == 1).cuda()]).all())
+    rows = np.nonzero(ids != 1)[0][::7]
+    check_adapters(got[torch.from_numpy(rows).cuda()], X[rows], w, up(down), up(upw), ids[rows], torch.tensor([3.4e38, 1.0]))
