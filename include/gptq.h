@@ -468,7 +468,8 @@ int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t
  * enters the second product as three bf16 numbers, which hold all of it.  What a row's
  * adapter holds reaches no other row.  Rows in any order; those of an adapter side
  * by side are fastest.  rank a multiple of 8, at most 128 (0: the product alone);
- * N at most 2^26; 16-byte aligned rows of X, codes and adapters (GPTQ_ERR_UNSUPPORTED).
+ * N at most 2^26, and no launch of 2^32 threads (weights or a Y of some 256 GB);
+ * 16-byte aligned rows of X, codes and adapters (GPTQ_ERR_UNSUPPORTED).
  * Needs workspace, as gptq_tree_attention: run once before a capture. */
 typedef struct {
   const uint16_t* down;

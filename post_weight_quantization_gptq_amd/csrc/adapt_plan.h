@@ -66,3 +66,18 @@ inline size_t adapt_part(const AdaptPlan& p, int M, int N) {
   return adapt_tiles(p, M, N) * p.parts * (p.shape == 1 ? 64 * 64 : 128 * 128) * sizeof(float);
 }
 inline size_t adapt_done(const AdaptPlan& p, int M, int N) { return adapt_tiles(p, M, N) * sizeof(int); }
+
+// Whether the threads of every launch can be counted in 32 bits.
+inline bool adapt_fits(const AdaptPlan& p, int M, int N, int K) {
+  static const struct {
+    int m, n, threads;
+  } tile[5] = {{64, 64, 256}, {128, 128, 512}, {128, 128, 512}, {128, 256, 512}, {256, 256, 512}};
+  const long long per = (K / 32 + 15) / 16;  // workgroups of 16 rows of X or of the weights
+  const long long down = (M + 31LL) / 32 * p.splits * p.slots + ((p.shape ? N : M) + 15LL) / 16 * per;
+  long long product = (N + 15LL) / 16 * 512;
+  if (p.shape) {
+    const auto& t = tile[p.shape - 1];
+    product = ((long long)M + t.m - 1) / t.m * (((long long)N + t.n - 1) / t.n) * p.parts * t.threads;
+  }
+  return down * 256 < 1LL << 32 && product < 1LL << 32;
+}

@@ -1640,7 +1640,11 @@ GPTQ_API int gptq_gemm_adapters(gptq_ctx c, const uint16_t* X, int64_t M, int64_
   p.gshift = gshift;
   p.count = any ? ad->count : 0;
   p.rank = any ? ad->rank : 0;
-  // 16384 rows at a time, which bounds the workspace
+  // 16384 rows at a time, which bounds the workspace; the last ones are planned by themselves
+  for (const int64_t rows : {std::min<int64_t>(M, 16384), M % 16384}) {
+    if (rows && !adapt_fits(plan_adapt((int)rows, N, K, c->ncu), (int)rows, N, K))
+      return set_err(c, GPTQ_ERR_UNSUPPORTED, "too many outputs and inputs for one launch");
+  }
   for (int64_t m = 0; m < M; m += 16384) {
     p.M = (int)std::min<int64_t>(M - m, 16384);
     p.X = X + m * ldx;

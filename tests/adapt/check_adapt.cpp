@@ -22,6 +22,10 @@ static void check_choice(int M, int N, int K, int shape, int parts) {
   CHECK(p.shape == shape && p.parts == parts, "%d x %d x %d: shape %d of %d workgroups", M, N, K, p.shape, p.parts);
 }
 
+static void check_refused(int M, int N, int K) {
+  CHECK(!adapt_fits(plan_adapt(M, N, K, 256), M, N, K), "%d x %d x %d: said to fit", M, N, K);
+}
+
 // What the kernels and their launches assume.
 static void check_limits(int M, int N, int K) {
   const AdaptPlan p = plan_adapt(M, N, K, 256);
@@ -32,10 +36,11 @@ static void check_limits(int M, int N, int K) {
         p.slots, p.splits);
   static const int side[6][2] = {{0, 0}, {64, 64}, {128, 128}, {128, 128}, {128, 256}, {256, 256}};
   const int threads = p.shape == 1 ? 256 : 512;
+  bool small = (N + 15LL) / 16 * 512 < 1LL << 32;
   if (p.shape) {
     const long long tiles = ((long long)M + side[p.shape][0] - 1) / side[p.shape][0] *
                             (((long long)N + side[p.shape][1] - 1) / side[p.shape][1]);
-    CHECK(tiles * p.parts * threads < 1LL << 32, "%d x %d x %d: %lld tiles of %d workgroups", M, N, K, tiles, p.parts);
+    small = tiles * p.parts * threads < 1LL << 32;
     CHECK(adapt_tiles(p, M, N) == (p.parts > 1 ? (size_t)tiles : 0), "%d x %d x %d: %zu counts", M, N, K, adapt_tiles(p, M, N));
     CHECK(adapt_part(p, M, N) == adapt_tiles(p, M, N) * p.parts * side[p.shape][0] * side[p.shape][1] * 4 &&
               adapt_done(p, M, N) == adapt_tiles(p, M, N) * 4,
@@ -43,7 +48,11 @@ static void check_limits(int M, int N, int K) {
   }
   const long long steps = K / 32, per = (steps + 15) / 16;
   const long long first = ((long long)M + 31) / 32 * p.splits * p.slots + ((p.shape ? N : M) + 15LL) / 16 * per;
-  CHECK(first * 256 < 1LL << 32, "%d x %d x %d: %lld workgroups of the first launch", M, N, K, first);
+  small = small && first * 256 < 1LL << 32;
+  CHECK(adapt_fits(p, M, N, K) == small, "%d x %d x %d: said to %s", M, N, K, small ? "be too large" : "fit");
+  // the weights as bf16 and Y take up to 200 GB
+  const long long bytes = (p.shape ? 2LL * N * K : 0) + 4LL * M * N;
+  CHECK(small || bytes > 200LL << 30, "%d x %d x %d: does not fit", M, N, K);
 }
 
 int main() {
@@ -74,11 +83,15 @@ int main() {
   check_choice(700, 3000, 32, 3, 1);
   check_choice(2000, 3800, 32, 4, 1);
   check_choice(2500, 4000, 32, 5, 1);
-  // sizes whose weights as bf16 and Y take up to 200 GB
+  // the refused ones of the GPU tests
+  check_refused(1000, 1 << 26, 0);
+  check_refused(200, 1 << 20, 1 << 17);
+  check_refused(16384, 1 << 20, 1 << 17);
+  check_refused(16384, 1 << 26, 32);
   for (int M : {1, 2, 16, 17, 100, 128, 129, 200, 999, 2048, 4096, 10000, 16384})
     for (int N : {1, 15, 64, 300, 2049, 4096, 11008, 14336, 128256, 1 << 20, 1 << 23, 1 << 26})
       for (int K : {0, 32, 96, 1024, 2048, 4096, 14336, 1 << 17, 1 << 22})
-        if ((M > 128 ? (long long)N * K * 2 : 0) + (long long)M * N * 4 < 200LL << 30) check_limits(M, N, K);
+        check_limits(M, N, K);
   if (g_fail) return 1;
   printf("adapter checks passed\n");
   return 0;

@@ -41,6 +41,7 @@ def test_sizes_take_the_kernels_that_the_tests_mean(tmp_path):
 MISTAKES = [
     ("a-tile-that-costs-more", "{128, 256, 62, 0}", "{128, 256, 90, 0}", "2048 x 4090 x 96"),
     ("sums-of-one-workgroup", "* p.parts * (p.shape == 1", "* (p.shape == 1", "bytes of sums"),
+    ("threads-of-a-launch-in-33-bits", "product < 1LL << 32;", "product < 1LL << 33;", "said to"),
     ("more-workgroups-than-rows", "std::min(M, 32))", "32)", "slots"),
 ]
 

@@ -1,11 +1,14 @@
 """A served step on the GPU where a hand-over, a border, a size or a rounding decides the result."""
+import ctypes
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from oracle import step_ref  # noqa: E402
-from post_weight_quantization_gptq_amd import Adapters, Context  # noqa: E402
+import post_weight_quantization_gptq_amd as gptq  # noqa: E402
+from post_weight_quantization_gptq_amd import Adapters, Context, GPTQError  # noqa: E402
 from test_gpu_step import (adapters_of, check_adapters, check_probabilities, check_verify, draft_case, f32, i32,  # noqa: E402
                            layer, rows_of, up)
 
@@ -302,3 +305,13 @@ def test_adapters_past_the_largest_bf16_on_every_tile(ctx, M, N, K):
     assert bool(torch.isposinf(got[torch.from_numpy(ids == 1).cuda()]).all())
     rows = np.nonzero(ids != 1)[0][::7]
     check_adapters(got[torch.from_numpy(rows).cuda()], X[rows], w, up(down), up(upw), ids[rows], torch.tensor([3.4e38, 1.0]))
+
+
+def test_adapters_of_more_outputs_than_a_launch_takes(ctx):
+    """Refused before anything is launched."""
+    x = torch.zeros(64, dtype=torch.bfloat16, device="cuda:0")
+    a, b = gptq._Adapters(None, None, None, 0, 0), x.data_ptr()
+    for M, N, K in ((1000, 1 << 26, 0), (200, 1 << 20, 1 << 17), (16384 + 200, 1 << 20, 1 << 17), (2 ** 31 - 1, 1 << 26, 32)):
+        with pytest.raises(GPTQError) as e:
+            ctx._check(ctx.lib.gptq_gemm_adapters(ctx.handle, b, M, K, b, b, b, N, K, 0, 4, ctypes.byref(a), b, b, N))
+        assert e.value.status == 4 and "launch" in str(e.value)
