@@ -9,8 +9,8 @@ torch = pytest.importorskip("torch")
 from oracle import step_ref  # noqa: E402
 import post_weight_quantization_gptq_amd as gptq  # noqa: E402
 from post_weight_quantization_gptq_amd import Adapters, Context, GPTQError  # noqa: E402
-from test_gpu_step import (adapters_of, check_adapters, check_probabilities, check_verify, draft_case, f32, i32,  # noqa: E402
-                           layer, rows_of, up)
+from test_gpu_step import (Tables, adapters_of, check_adapters, check_probabilities, check_verify,  # noqa: E402
+                           draft_case, f32, i32, layer, rows_of, up)
 
 pytestmark = pytest.mark.gpu
 
@@ -315,3 +315,51 @@ def test_adapters_of_more_outputs_than_a_launch_takes(ctx):
         with pytest.raises(GPTQError) as e:
             ctx._check(ctx.lib.gptq_gemm_adapters(ctx.handle, b, M, K, b, b, b, N, K, 0, 4, ctypes.byref(a), b, b, N))
         assert e.value.status == 4 and "launch" in str(e.value)
+
+
+# ------------------------------------------------- the largest of each --
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_probabilities_of_more_rows_than_a_launch_takes(ctx, dtype):
+    """2^22 rows and some more, every fourth greedy; one row of 2^22 values."""
+    seqs = (1 << 22) + 37
+    x = torch.randn((seqs, 5), generator=torch.Generator(device="cuda:0").manual_seed(1), device="cuda:0").to(dtype)
+    t = torch.ones(seqs, device="cuda:0")
+    t[3::4] = 0.0
+    p = ctx.probabilities(x, t).double()
+    want = torch.softmax(x.double(), -1)
+    first = torch.where(x == x.amax(-1, keepdim=True), torch.arange(5, device="cuda:0"), 5).amin(-1, keepdim=True)
+    want[3::4] = (torch.arange(5, device="cuda:0") == first).double()[3::4]
+    assert float(((p - want).abs() / want.clamp(min=1e-30)).max()) <= 100 * U
+    row = torch.randn((1, 1 << 22), generator=torch.Generator(device="cuda:0").manual_seed(2), device="cuda:0").to(dtype)
+    row[0, -1] = 9.0
+    p = ctx.probabilities(row).double()
+    want = torch.softmax(row.double(), -1)
+    assert float(((p - want).abs() / want).max()) <= (4096 * 19 / 16 + 150) * U
+    assert int(ctx.probabilities(row, torch.zeros(1, device="cuda:0")).argmax()) == (1 << 22) - 1
+
+
+def test_verify_of_many_sequences(ctx):
+    check_verify(ctx, draft_case(np.random.default_rng(47), 3000, 4, 23, True, True))
+    check_verify(ctx, draft_case(np.random.default_rng(48), 700, 3, 8200, False, True))
+
+
+@pytest.mark.parametrize("seqs,width", [(8192, 5), (8191, 2), (4100, 20)])
+def test_tables_of_many_sequences(ctx, seqs, width):
+    page = 32
+    t = Tables(ctx, seqs * width, seqs, width, page)
+    g = np.random.default_rng(seqs)
+    lengths = np.zeros(seqs, np.int64)
+    for _ in range(3):
+        added = g.integers(-3, width * page // 4, seqs)
+        _, info = t.extend(lengths, added)
+        assert info[1] == 0
+        lengths += np.maximum(added, 0)
+        rows = g.permutation(seqs)
+        t.fork(lengths, rows[:seqs // 2], rows[seqs // 2:2 * (seqs // 2)])
+        lengths[rows[seqs // 2:2 * (seqs // 2)]] = lengths[rows[:seqs // 2]]
+        t.consistent()
+    lengths[::3] = 0
+    t.free(lengths)
+    t.consistent()
+    t.extend(lengths, np.full(seqs, width * page))  # past the tables: nothing changes
+    t.consistent()
