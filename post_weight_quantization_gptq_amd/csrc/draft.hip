@@ -192,11 +192,13 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, a[k].get(i));
     const float from = base(top) * half;
-    l *= power(m, from);
+    // (four sums of a chunk, then those: 4 roundings of few values, not 16 of all so far)
+    float of[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < decltype(n)::value; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l += power(a[k].get(i), from);
+      for (int i = 0; i < 4; ++i) of[i] += power(a[k].get(i), from);
+    l = fmaf(l, power(m, from), (of[0] + of[1]) + (of[2] + of[3]));
     m = top;
   };
   std::integral_constant<int, 1> one;
