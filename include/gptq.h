@@ -470,7 +470,11 @@ int gptq_tree_attention(gptq_ctx ctx, const gptq_kv_cache* cache, const uint16_t
  * by side are fastest.  rank a multiple of 8, at most 128 (0: the product alone);
  * N at most 2^26, and no launch of 2^32 threads (weights or a Y of some 256 GB);
  * 16-byte aligned rows of X, codes and adapters (GPTQ_ERR_UNSUPPORTED).
- * Needs workspace, as gptq_tree_attention: run once before a capture. */
+ * Needs workspace, as gptq_tree_attention: run once before a capture.  Above 128 rows that
+ * is a bf16 copy of the whole layer, 2 N K bytes (1 GB for 128256 x 4096), and up to
+ * 150 MB of sums where several workgroups have a tile; for fewer rows 2 M K; and 4 to 16 M
+ * rank bytes (M at most 16384).  The context keeps the largest so far, or twice the one
+ * before it, and what it has outgrown, until gptq_destroy. */
 typedef struct {
   const uint16_t* down;
   const uint16_t* up;

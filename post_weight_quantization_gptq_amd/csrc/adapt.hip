@@ -1,8 +1,8 @@
 // The quantised product with a low-rank adapter for every row (gfx950):
 //   Y = X What^T + alpha_a (X down_a^T) up_a^T,  a = ids[row]
-// in two launches: T = alpha_a X down_a^T into workspace (and, for many rows, the
-// weights as bf16), then the product with the adapters' second half added to its
-// sums before they are stored.
+// in two launches: T = X down_a^T into workspace (and, for many rows, the weights as
+// bf16), then the product with alpha_a T up_a^T added to its sums before they are
+// stored.
 #include "common.h"
 #include "adapt.h"
 
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * AD_W) void k_adapt_down(const AdaptProb p) {
 // which are its k in four products; X lies in that order.  The (16 rows, adapter) pairs are
 // shared out among the waves, too; all sums are added in LDS in order.  Bound by waits on
 // X, which every workgroup reads (64 rows of 4096 x 4096: 134 MB from the L2s): 64 rows at
-// 4 bits with 48 adapters of rank 16 15 us; one row of 2048 x 6144 at 3 bits 8.4 us.
+// 4 bits with 48 adapters of rank 16 15.7 us; one row of 2048 x 6144 at 3 bits 8.5 us.
 template <int BITS, int RB, int CB, int NW>
 __global__ __launch_bounds__(64 * NW) void k_adapt_rows(const AdaptProb p) {
   constexpr int PAIRS = 16 * RB, MINE = (PAIRS + NW - 1) / NW, AT = MINE < 8 ? MINE : 8;
@@ -456,8 +456,8 @@ __global__ __launch_bounds__(64 * NW) void k_adapt_rows(const AdaptProb p) {
 // product alone: 110 us, on 32x32x16 117; the power limit bounds both, 92 us on zeros); KH
 // k-steps of 32 a stage of LDS, in a ring of NS stages filled NS - 1 ahead.  One barrier
 // a stage.  The fragments of a step are read beside the products of the one before.
-// With 4096 rows of five adapters of rank 32 115 us, 1.19 PFLOP/s; 999 rows of 16 adapters
-// of rank 64, 6144 x 2048, 42 us (47 when one of a tile's two had the adapters' part).
+// With 4096 rows of five adapters of rank 32 114 to 122 us by card, 1.2 PFLOP/s; 999 rows of
+// 16 adapters of rank 64, 6144 x 2048, 40 us.
 // SPLIT: parts workgroups have a tile, a share of k and of the adapters' part each; the one
 // that is done last adds all sums in order and stores them.
 template <int BM, int BN, int WM, int WN, int KH, int NS, bool SPLIT>
@@ -791,7 +791,7 @@ template <int BITS>
 hipError_t product_bits(const AdaptProb& p, hipStream_t st) {
   if (!p.shape) {
     // 64 rows of 4096 outputs (256 workgroups) 21 us, by 32 outputs 25; 128 rows 38 and 26; 89
-    // rows of 715 16 and 24
+    // rows of 715 16 and 24.  (Up to 64 rows of more outputs: by 16 as well, 32 not measured.)
     if (p.M <= 16)
       rows_shape<BITS, 1, 1, 8>(p, st);
     else if (p.M <= 32)

@@ -1726,7 +1726,8 @@ GPTQ_API int gptq_verify_draft(gptq_ctx c, const float* P, int64_t p_seq, int64_
   const int tiles = verify_tiles(vocab);
   p.split = std::min(tiles, std::max(c->ncu / seqs, 1));
   // launches: one where no second sum is wanted or a workgroup has a whole sequence; a
-  // sum alone takes 18 us of 131072 values, in a launch 11, and a launch without one 2
+  // sum alone takes 18 us of 131072 values, in a launch 11, and a launch without one 2 (below
+  // 65536 values one launch would take less: see k_verify)
   p.launches = Q && parents && p.split > 1 ? std::min(6, std::max(tokens - 1, 1)) : 1;
   if (p.split > 1) {
     const size_t sums = (size_t)seqs * tiles * sizeof(double);

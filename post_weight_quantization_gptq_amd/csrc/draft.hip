@@ -20,10 +20,12 @@ __device__ __forceinline__ void load_any(const float* p, float* o) {
 // t = 0: 1 at the first maximum.  A row with a NaN or +infinity (t > 0), or a
 // temperature below 0 or not finite, is NaN; a row of -infinity alone is zero.
 // A workgroup has a row, which stays in its registers from the load on: 4 C values a
-// thread, as they came.  Rows that are longer are read in such blocks, once for each use.
+// thread, as they came.  Rows that are longer (fp32 past 65536 values, bf16 past 131072) are
+// read in such blocks twice, for the sum and for the result.
 // Bound by HBM where there are rows for the CUs: 208 rows of 100003 bf16 values, 125 MB in
-// 23.8 us, 5.3 TB/s (31.5 with the sum behind the largest value, 62 with the row read
-// twice); five rows of 32768 fp32 values, one CU each, 6.3 us.
+// 24.8 us, 5.0 TB/s (31.5 with the sum behind the largest value), of 65536 fp32 values 109 MB
+// in 21.7 us; read twice, 208 rows of 100003 fp32 values 36 us, of 131072 46.5, of 200003 bf16
+// values 52.  Five rows of 32768 fp32 values, one CU each, 7.4 us.
 namespace {
 
 template <class T>
@@ -270,7 +272,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(NT / 256, 4)
 // goes on with all of them, alone.  A chain ends there; a tree wants a sum more for
 // every rejected child that has siblings: each in a launch of its own, as far as the
 // launches go (131072 values: 11 us, 18 us where a workgroup has all of them, which 64-bit
-// arithmetic bounds).
+// arithmetic bounds).  Where the vocabulary is small the launches cost more than they save:
+// 16 trees of 27 nodes over 8192 values 57 to 70 us by seed, 28 to 39 in one launch; 32768: 46
+// to 91 and 28 to 69; 65536: 63 to 83 and 59 to 79; 131072: 50 to 80 and 65 to 113.
 // Bound by latency: a chain over 32768 values takes 11.4 us, of which the nodes' values
 // are 2.4, the walk 1.6, the sums 2.3, their hand-over 2.1 and the draw 3.1; 16 trees of 27
 // nodes over 131072 values 53 to 119 us, by how many sums they want.
