@@ -491,7 +491,8 @@ int gptq_gemm_adapters(gptq_ctx ctx, const uint16_t* X, int64_t M, int64_t ldx, 
  * first maximum, 0 elsewhere.  A row of -infinity alone is zero; a row with a NaN,
  * with +infinity (temperature above 0), or whose temperature is negative or not
  * finite is NaN.  Strides in elements, the vocabulary contiguous; P must not
- * overlap the logits.  vocab at most 2^22. */
+ * overlap the logits, nor its rows each other (one stride at least vocab, the other past
+ * all rows of the first: GPTQ_ERR_INVALID_ARG).  vocab at most 2^22. */
 int gptq_probabilities(gptq_ctx ctx, const void* logits, int32_t type, int64_t seqs, int32_t tokens, int32_t vocab,
                        int64_t x_seq, int64_t x_token, const float* temperature, float* P, int64_t p_seq,
                        int64_t p_token);

@@ -1684,6 +1684,10 @@ GPTQ_API int gptq_probabilities(gptq_ctx c, const void* logits, int32_t type, in
     return set_err(c, GPTQ_ERR_UNSUPPORTED, "buffers must be aligned to their type");
   if (seqs == 1) x_seq = p_seq = 0;  // the stride of a dimension of one is never used
   if (tokens == 1) x_token = p_token = 0;
+  // the rows along one dimension, and all of those along the other
+  if ((tokens > 1 && p_token < vocab) || (seqs > 1 && p_seq < vocab) ||
+      (tokens > 1 && seqs > 1 && (p_seq - vocab) / (tokens - 1) < p_token && (p_token - vocab) / (seqs - 1) < p_seq))
+    return set_err(c, GPTQ_ERR_INVALID_ARG, "rows of P overlap");
   DeviceGuard g(c->device);
   const ProbsProb p{logits, P, temperature, seqs, x_seq, x_token, p_seq, p_token, tokens, vocab};
   LAUNCH(c, "k_probs", launch_probabilities(p, type, c->stream));

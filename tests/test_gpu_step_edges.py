@@ -222,6 +222,22 @@ def test_every_value_counts(ctx, vocab, dtype):
     assert float((p[x[0] == 1] * (vocab - 1) - 1).abs().max()) <= (vocab / 256 + 60) * U
 
 
+def test_probabilities_into_rows_that_overlap(ctx):
+    """Refused; sequences and tokens in either order, side by side or apart, are not."""
+    x = torch.randn((4, 3, 10), generator=torch.Generator().manual_seed(9)).cuda()
+    buf = torch.zeros(1000, device="cuda:0")
+    want = ctx.probabilities(x)
+    for seq, token in ((30, 10), (10, 40), (31, 10), (100, 33), (11, 44), (10, 45)):
+        assert torch.equal(ctx.probabilities(x, out=buf.as_strided((4, 3, 10), (seq, token, 1))), want)
+    for seq, token in ((0, 10), (30, 0), (29, 10), (30, 9), (10, 39), (9, 40), (10, 10), (0, 0)):
+        with pytest.raises(GPTQError) as e:
+            ctx.probabilities(x, out=buf.as_strided((4, 3, 10), (seq, token, 1)))
+        assert e.value.status == 1
+    assert torch.equal(ctx.probabilities(x[:1], out=buf.as_strided((1, 3, 10), (0, 10, 1))), want[:1])
+    assert torch.equal(ctx.probabilities(x[:, :1], out=buf.as_strided((4, 1, 10), (10, 0, 1))), want[:, :1])
+    assert torch.equal(ctx.probabilities(x[:1, 0], out=buf.as_strided((1, 10), (3, 1))), want[:1, 0])
+
+
 # ------------------------------------------------------------- adapters --
 # few rows (16, 32, 64, 128, 128 of many outputs), then a size for every tile, 64 x 64 by one and by several workgroups
 KERNELS = [(3, 40, 32), (30, 200, 64), (60, 333, 160), (100, 500, 32), (128, 2100, 96), (200, 700, 64), (200, 700, 2048),
